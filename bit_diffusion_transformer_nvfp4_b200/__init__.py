@@ -27,6 +27,8 @@ __all__ = [
     "gemm_swiglu", "w4a4_gemm_quantize_next", "gemm_quantize_next", "w4a4_gemm_rope", "gemm_rope",
     "fp8_quant_workspace_bytes", "fp8_quantize", "attention_fp8", "Fp8Tensor", "quantize_fp8", "attention",
     "w4a4_fp4_mma_rate", "w4a4_last_error", "MAX_K",
+    "fp8_quantize_rows", "rmsnorm_fp8", "fp8_gemm", "cross_attention_bf16", "Fp8Rows", "PackedWeightFp8",
+    "quantize_rows_fp8", "rms_norm_fp8", "pack_weight_fp8", "linear_fp8", "cross_attention", "MAX_ROW_COLS",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -35,6 +37,7 @@ LIB_PATH = os.path.join(HERE, "libw4a4.so")
 EPI_NONE, EPI_GELU_TANH = 0, 1
 SRC_BF16, SRC_F32 = 0, 1
 MAX_K = 1 << 20  # W4A4_MAX_K: the widest K (activation or weight columns) the entry points accept
+MAX_ROW_COLS = 32768  # W4A4_MAX_ROW_COLS: the widest row of the row quantiser and the norm
 
 _c = ctypes
 _P = _c.c_void_p
@@ -61,6 +64,12 @@ _SIG = {
     "fp8_quantize": (_c.c_int, [_P, _I64, _I64, _I64, _c.c_int, _P, _I64, _P, _P, _c.c_size_t, _P]),
     "attention_fp8": (_c.c_int, [_P, _P, _P, _I64, _I64, _I64, _I64, _I64, _I64, _P, _P, _P, _c.c_float, _P, _I64,
                                  _P]),
+    "fp8_quantize_rows": (_c.c_int, [_P, _I64, _I64, _I64, _P, _I64, _P, _P]),
+    "rmsnorm_fp8": (_c.c_int, [_P, _I64, _I64, _I64, _P, _I64, _P, _c.c_float, _P, _I64, _P, _I64, _P, _I64, _P, _P]),
+    "fp8_gemm": (_c.c_int, [_P, _I64, _P, _c.c_int, _I64, _I64, _I64, _P, _I64, _P, _P, _c.c_int, _P, _I64, _P, _I64,
+                            _P]),
+    "cross_attention_bf16": (_c.c_int, [_P, _I64, _P, _I64, _P, _I64, _I64, _I64, _I64, _I64, _I64, _I64, _I64, _P, _P,
+                                        _I64, _c.c_float, _P, _I64, _P]),
     "w4a4_gemm_quantize_next": (_c.c_int, [_P, _P, _P, _P, _I64, _I64, _I64, _P, _P, _P, _P, _c.c_int, _P,
                                            _c.c_int, _I64, _P, _I64, _P, _I64, _P, _P, _P, _I64, _P, _I64, _I64,
                                            _P, _P]),
@@ -209,6 +218,30 @@ def attention_fp8(Q8, K8, Vt8, batch, S, heads, ldq, ldk, ldvt, s_q, s_k, s_v, s
     _check("attention_fp8", lib().attention_fp8(
         _ptr(Q8), _ptr(K8), _ptr(Vt8), batch, S, heads, ldq, ldk, ldvt, _ptr(s_q), _ptr(s_k), _ptr(s_v),
         float(softmax_scale), _ptr(O), ldo, _stream(stream)))
+
+
+def fp8_quantize_rows(X, rows, cols, ldx, codes, ldo, scales, stream=None):
+    _check("fp8_quantize_rows", lib().fp8_quantize_rows(
+        _ptr(X), rows, cols, ldx, _ptr(codes), ldo, _ptr(scales), _stream(stream)))
+
+
+def rmsnorm_fp8(X, rows, cols, ldx, R, ldr, weight, eps, hidden, ldh, normed, ldn, codes, ldo, scales, stream=None):
+    _check("rmsnorm_fp8", lib().rmsnorm_fp8(
+        _ptr(X), rows, cols, ldx, _ptr(R), ldr, _ptr(weight), float(eps), _ptr(hidden), ldh, _ptr(normed), ldn,
+        _ptr(codes), ldo, _ptr(scales), _stream(stream)))
+
+
+def fp8_gemm(A8, lda, s_a, s_a_rows, M, N, K, W8, ldw, s_w, bias, epilogue, R, ldr, Y, ldy, stream=None):
+    _check("fp8_gemm", lib().fp8_gemm(
+        _ptr(A8), lda, _ptr(s_a), s_a_rows, M, N, K, _ptr(W8), ldw, _ptr(s_w), _ptr(bias), epilogue, _ptr(R), ldr,
+        _ptr(Y), ldy, _stream(stream)))
+
+
+def cross_attention_bf16(Q, ldq, K, ldk, V, ldv, batch, kv_batch, Sq, Skv, heads, kv_heads, d_head, kv_len, key_mask,
+                         ld_mask, softmax_scale, O, ldo, stream=None):
+    _check("cross_attention_bf16", lib().cross_attention_bf16(
+        _ptr(Q), ldq, _ptr(K), ldk, _ptr(V), ldv, batch, kv_batch, Sq, Skv, heads, kv_heads, d_head, _ptr(kv_len),
+        _ptr(key_mask), ld_mask, float(softmax_scale), _ptr(O), ldo, _stream(stream)))
 
 
 def w4a4_gemm_quantize_next(Xq, Xsf, t_x, U, M, N, K, Wq, Wsf, t_w, L2t, r, bias, epilogue, n_plain, Y, ldy, H,
@@ -421,6 +454,185 @@ def attention(q: Fp8Tensor, k: Fp8Tensor, vt: Fp8Tensor, heads: int, batch: int 
     c = 1.0 / math.sqrt(128.0) if softmax_scale is None else softmax_scale
     attention_fp8(q.codes, k.codes, vt.codes, batch, S, heads, q.codes.stride(0), k.codes.stride(0),
                   vt.codes.stride(0), q.scale, k.scale, vt.scale, c, O, O.stride(0), stream)
+    return O
+
+
+def _matrix(name, t, dtype, rows=None, cols=None, device=None):
+    """The row stride of a 2-D tensor of the given type whose rows are
+    contiguous; raises on anything the kernels would misread."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: {dtype} expected, got {t.dtype}")
+    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
+        raise ValueError(f"{name}: shape [{'*' if rows is None else rows}, {'*' if cols is None else cols}] expected, "
+                         f"got {list(t.shape)}")
+    if t.device.type != "cuda" or (device is not None and t.device != device):
+        raise ValueError(f"{name}: on {t.device}, expected {device or 'a CUDA device'}")
+    r, c = t.shape
+    if c > 1 and t.stride(1) != 1 or r > 1 and t.stride(0) < c:
+        raise ValueError(f"{name}: contiguous rows expected, got strides {t.stride()}")
+    return t.stride(0) if r > 1 else -(-c // 16) * 16  # (one row: its stride never matters)
+
+
+def _vector(name, t, dtype, n, device):
+    if t.dtype != dtype or t.shape != (n,) or t.device != device or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name}: contiguous {dtype} [{n}] on {device} expected, got {t.dtype} {list(t.shape)} with "
+                         f"strides {t.stride()} on {t.device}")
+
+
+class _on:
+    """Makes a tensor's device current for a call (the library works on the
+    current device)."""
+
+    def __init__(self, device):
+        self.index = device.index
+        self.back = None
+
+    def __enter__(self):
+        if torch.cuda.current_device() != self.index:
+            self.back = torch.cuda.current_device()
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *exc):
+        if self.back is not None:
+            torch.cuda.set_device(self.back)
+
+
+class Fp8Rows:
+    """E4M3 codes (uint8 [rows, cols]) with one fp32 scale per row."""
+
+    def __init__(self, codes, scales):
+        self.codes, self.scales = codes, scales
+        self.rows, self.cols = codes.shape
+
+
+class PackedWeightFp8:
+    """An FP8 linear layer: the weight's E4M3 codes (uint8 [N, K]), one fp32
+    scale per output channel, an optional bf16 bias [N]."""
+
+    def __init__(self, codes, scales, bias=None):
+        self.codes, self.scales, self.bias = codes, scales, bias
+        self.N, self.K = codes.shape
+
+
+def quantize_rows_fp8(X, codes=None, scales=None, stream=None) -> Fp8Rows:
+    """E4M3 codes of a bf16 [rows, cols] view, one scale per row (cols a
+    multiple of 8, at most MAX_ROW_COLS)."""
+    ldx = _matrix("X", X, torch.bfloat16)
+    rows, cols = X.shape
+    dev = X.device
+    if codes is None:
+        codes = torch.empty(rows, cols, dtype=torch.uint8, device=dev)
+    if scales is None:
+        scales = torch.empty(rows, dtype=torch.float32, device=dev)
+    ldo = _matrix("codes", codes, torch.uint8, rows, cols, dev)
+    _vector("scales", scales, torch.float32, rows, dev)
+    with _on(dev):
+        fp8_quantize_rows(X, rows, cols, ldx, codes, ldo, scales, stream)
+    return Fp8Rows(codes, scales)
+
+
+def rms_norm_fp8(X, weight=None, residual=None, eps=1e-6, hidden=None, normed=None, codes=None, scales=None,
+                 stream=None):
+    """E4M3 row codes of the root-mean-square norm of X + residual (bf16
+    [rows, cols] views), times ``weight`` (bf16 [cols]).  Returns (Fp8Rows,
+    hidden): hidden is bf16(X + residual), written when a residual is given
+    (in place with ``hidden=X`` or ``hidden=residual``), else None unless a
+    tensor is passed.  ``normed``: a bf16 tensor that also receives the norm
+    itself, for a W4A4 layer behind it (``quantize_act``)."""
+    ldx = _matrix("X", X, torch.bfloat16)
+    rows, cols = X.shape
+    dev = X.device
+    ldr = ldh = ldn = 0
+    if residual is not None:
+        ldr = _matrix("residual", residual, torch.bfloat16, rows, cols, dev)
+        if hidden is None:
+            hidden = torch.empty(rows, cols, dtype=torch.bfloat16, device=dev)
+    if hidden is not None:
+        ldh = _matrix("hidden", hidden, torch.bfloat16, rows, cols, dev)
+    if normed is not None:
+        ldn = _matrix("normed", normed, torch.bfloat16, rows, cols, dev)
+    if weight is not None:
+        _vector("weight", weight, torch.bfloat16, cols, dev)
+    if codes is None:
+        codes = torch.empty(rows, cols, dtype=torch.uint8, device=dev)
+    if scales is None:
+        scales = torch.empty(rows, dtype=torch.float32, device=dev)
+    ldo = _matrix("codes", codes, torch.uint8, rows, cols, dev)
+    _vector("scales", scales, torch.float32, rows, dev)
+    with _on(dev):
+        rmsnorm_fp8(X, rows, cols, ldx, residual, ldr, weight, eps, hidden, ldh, normed, ldn, codes, ldo, scales,
+                    stream)
+    return Fp8Rows(codes, scales), hidden
+
+
+def pack_weight_fp8(W, bias=None, stream=None) -> PackedWeightFp8:
+    """A bf16 weight [N, K] as an FP8 linear layer (one scale per output channel)."""
+    a = quantize_rows_fp8(W, stream=stream)
+    return PackedWeightFp8(a.codes, a.scales, bias)
+
+
+def linear_fp8(a, w: PackedWeightFp8, activation: int = EPI_NONE, residual=None, Y=None, stream=None):
+    """Y = activation(a w^T + bias) + residual in bf16 [rows, N], on E4M3
+    codes: ``a`` an Fp8Rows (a scale per row) or a row-major Fp8Tensor (one
+    scale).  ``Y`` may be ``residual`` itself."""
+    per_row = isinstance(a, Fp8Rows)
+    if not per_row and a.transposed:
+        raise ValueError("a: row-major codes expected")
+    codes = a.codes
+    lda = _matrix("a.codes", codes, torch.uint8, None, w.K)
+    M, dev = codes.shape[0], codes.device
+    ldw = _matrix("w.codes", w.codes, torch.uint8, w.N, w.K, dev)
+    s_a = a.scales if per_row else a.scale
+    _vector("a.scales", s_a, torch.float32, M if per_row else 1, dev)
+    _vector("w.scales", w.scales, torch.float32, w.N, dev)
+    if w.bias is not None:
+        _vector("w.bias", w.bias, torch.bfloat16, w.N, dev)
+    ldr = 0
+    if residual is not None:
+        ldr = _matrix("residual", residual, torch.bfloat16, M, w.N, dev)
+    if Y is None:
+        Y = torch.empty(M, w.N, dtype=torch.bfloat16, device=dev)
+    ldy = _matrix("Y", Y, torch.bfloat16, M, w.N, dev)
+    with _on(dev):
+        fp8_gemm(codes, lda, s_a, int(per_row), M, w.N, w.K, w.codes, ldw, w.scales, w.bias, activation, residual,
+                 ldr, Y, ldy, stream)
+    return Y
+
+
+def cross_attention(q, k, v, heads: int, kv_heads=None, batch: int = 1, kv_batch=None, kv_len=None, key_mask=None,
+                    O=None, softmax_scale=None, stream=None):
+    """Attention of ``batch`` sequences of q.shape[0] / batch tokens to
+    ``kv_batch`` (default: batch; 1: shared by all) sequences of keys and
+    values of another length: bf16 views q [batch*Sq, heads*d], k and v
+    [kv_batch*Skv, kv_heads*d], d a multiple of 8 up to 128.  ``kv_len``:
+    int32 [kv_batch], the keys that count; ``key_mask``: bool or uint8
+    [kv_batch, Skv], False for keys that do not.  Returns bf16 O
+    [batch*Sq, heads*d]; a query without keys gets 0."""
+    kv_heads = heads if kv_heads is None else kv_heads
+    kv_batch = batch if kv_batch is None else kv_batch
+    ldq = _matrix("q", q, torch.bfloat16)
+    dev = q.device
+    if heads < 1 or kv_heads < 1 or batch < 1 or kv_batch < 1 or q.shape[1] % heads or q.shape[0] % batch:
+        raise ValueError(f"q {list(q.shape)} does not divide into {batch} sequences of {heads} heads")
+    d, Sq = q.shape[1] // heads, q.shape[0] // batch
+    ldk = _matrix("k", k, torch.bfloat16, None, kv_heads * d, dev)
+    if k.shape[0] % kv_batch:
+        raise ValueError(f"k {list(k.shape)} does not divide into {kv_batch} sequences")
+    Skv = k.shape[0] // kv_batch
+    ldv = _matrix("v", v, torch.bfloat16, k.shape[0], kv_heads * d, dev)
+    if kv_len is not None:
+        _vector("kv_len", kv_len, torch.int32, kv_batch, dev)
+    ldm = 0
+    if key_mask is not None:
+        ldm = max(Skv, _matrix("key_mask", key_mask, torch.uint8 if key_mask.dtype == torch.uint8 else torch.bool,
+                               kv_batch, Skv, dev))
+    if O is None:
+        O = torch.empty(q.shape[0], heads * d, dtype=torch.bfloat16, device=dev)
+    ldo = _matrix("O", O, torch.bfloat16, q.shape[0], heads * d, dev)
+    c = 1.0 / math.sqrt(d) if softmax_scale is None else softmax_scale
+    with _on(dev):
+        cross_attention_bf16(q, ldq, k, ldk, v, ldv, batch, kv_batch, Sq, Skv, heads, kv_heads, d, kv_len, key_mask,
+                             ldm, c, O, ldo, stream)
     return O
 
 

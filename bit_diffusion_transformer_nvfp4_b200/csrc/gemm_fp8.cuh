@@ -1,0 +1,450 @@
+// gemm_fp8.cuh -- the FP8 linear layer: E4M3 codes of both operands with one
+// fp32 scale per row of each, and bias, activation and residual in the
+// epilogue,
+//   Y[m,n] = bf16( act( s_a[m] s_w[n] sum_k dec(A[m,k]) dec(W[n,k]) + bias[n] ) + R[m,n] ).
+// The scales are constant along k, so the products run on the codes as they
+// are (tcgen05.mma kind::f8f6f4, fp32 accumulation in TMEM) and the scales
+// multiply the finished sum.
+//
+// Two kernels:
+//   gemm_fp8_pair_kernel   many rows: persistent CTA pairs, 256 x BN tiles,
+//                          bound by the FP8 tensor pipe.
+//   gemm_fp8_small_kernel  few rows: bound by streaming the weight once, so
+//                          the weight rows are the 128-row operand, the
+//                          tokens the narrow one, K is split over a cluster
+//                          and the partial sums meet in shared memory.
+#pragma once
+
+#include "attention.cuh"
+#include "gemm.cuh"
+#include "sm100.cuh"
+
+namespace w4a4 {
+
+struct Fp8GemmParams {
+  int M, N, K;
+  const float* s_a;
+  int s_a_step;              // 1: one scale per row of A, 0: one for all
+  const float* s_w;
+  const __nv_bfloat16* bias; // or nullptr
+  const __nv_bfloat16* R;    // or nullptr
+  __nv_bfloat16* Y;
+  int64_t ldr, ldy;
+  int epi;
+  int* status;
+};
+
+__device__ __forceinline__ void mma_e4m3_pair(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                              uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// ------------------------------------------------------------------ many rows
+// Two SMs share a 256 x BN tile; each CTA loads its 128 rows of A and BN / 2
+// rows of W per 128-deep K step (128-byte swizzled boxes; past the end of K
+// TMA fills zeros).  TMEM holds two accumulators, so the epilogue of a tile
+// runs under the next tile's products.  Warp 0 TMA producer, warp 1 TMEM
+// owner and (even CTA) MMA issuer, warps 2-3 spare, warps 4-11 epilogue: a
+// warp owns 32 rows x BN / 2 columns and a staging box of 32 x 32 bf16 per 32
+// columns, which receives the residual by TMA while the products run, is
+// overwritten in place and leaves by a TMA store.
+template <int BN_, int STAGES_>
+struct Fp8PairCfg {
+  static constexpr int BN = BN_, BH = BN / 2, STAGES = STAGES_;
+  static constexpr int BM = 128, BK = 128;
+  static constexpr int A_BYTES = BM * BK, B_BYTES = BH * BK, STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr int NUM_ACC = 2;
+  static constexpr int TMEM_COLS = NUM_ACC * BN;
+  static constexpr int EPI_WARPS = 8, EPI_WARP0 = 4;
+  static constexpr int THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
+  static constexpr int HALF = BN / 2, BOXES = HALF / 32;
+  static constexpr int BOX_BYTES = 32 * 64;
+  static constexpr int EPI_BYTES = EPI_WARPS * BOXES * BOX_BYTES;
+  static constexpr int BAR_BYTES = (8 * (2 * STAGES + 2 * NUM_ACC + EPI_WARPS + 1) + 8 + 127) / 128 * 128;
+  static constexpr int SMEM = STAGE_BYTES * STAGES + EPI_BYTES + BAR_BYTES + 1024;
+  static_assert(SMEM <= 232448, "shared memory budget");
+  static_assert(TMEM_COLS <= 512 && (TMEM_COLS & (TMEM_COLS - 1)) == 0, "TMEM budget");
+  static_assert(HALF % 32 == 0 && STAGE_BYTES % 1024 == 0, "tile shape");
+};
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, 1)
+    gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w,
+                         const __grid_constant__ CUtensorMap tm_r, const __grid_constant__ CUtensorMap tm_y,
+                         const Fp8GemmParams p) {
+  constexpr int BN = C::BN, STAGES = C::STAGES;
+  grid_launch_dependents();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* epi_smem = smem + C::STAGE_BYTES * STAGES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(epi_smem + C::EPI_BYTES);
+  uint64_t* empty = full + STAGES;
+  uint64_t* acc_full = empty + STAGES;
+  uint64_t* acc_empty = acc_full + C::NUM_ACC;
+  uint64_t* res_full = acc_empty + C::NUM_ACC;  // [EPI_WARPS] the warp's residual boxes have landed
+  uint64_t* drain = res_full + C::EPI_WARPS;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), 1);
+    }
+    for (int a = 0; a < C::NUM_ACC; ++a) {
+      mbar_init(smem_u32(&acc_full[a]), 1);
+      mbar_init(smem_u32(&acc_empty[a]), 2 * C::EPI_WARPS);
+    }
+    for (int w = 0; w < C::EPI_WARPS; ++w) mbar_init(smem_u32(&res_full[w]), 1);
+    mbar_init(smem_u32(drain), 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tm_a);
+    tma_prefetch_desc(&tm_w);
+    tma_prefetch_desc(&tm_y);
+    if (p.R != nullptr) tma_prefetch_desc(&tm_r);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(tmem_slot), C::TMEM_COLS);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync();  // both CTAs' barriers are initialised before any remote use
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  grid_dependency_wait();
+
+  const int m_tiles = (p.M + 2 * C::BM - 1) / (2 * C::BM);
+  const int n_tiles = (p.N + BN - 1) / BN;
+  const int total = m_tiles * n_tiles;
+  const int nkb = (p.K + C::BK - 1) / C::BK;
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ A/W producer (both CTAs)
+    if (lane == 0) {
+      uint32_t it = 0;
+      bool ok = true;
+      for (int tile = pair; tile < total && ok; tile += pairs) {
+        const int m0 = (tile % m_tiles) * 2 * C::BM + static_cast<int>(rank) * C::BM;
+        const int n0 = (tile / m_tiles) * BN + static_cast<int>(rank) * C::BH;
+        for (int kb = 0; kb < nkb; ++kb, ++it) {
+          const int s = it % STAGES;
+          if (!mbar_wait(smem_u32(&empty[s]), ((it / STAGES) & 1) ^ 1, abort_flag, p.status)) { ok = false; break; }
+          uint8_t* st = smem + s * C::STAGE_BYTES;
+          const uint32_t bar = mapa_shared(smem_u32(&full[s]), 0);
+          if (leader) mbar_arrive_expect_tx(smem_u32(&full[s]), 2 * C::STAGE_BYTES);
+          tma_load_2d_pair(smem_u32(st), &tm_a, bar, kb * C::BK, m0);
+          tma_load_2d_pair(smem_u32(st + C::A_BYTES), &tm_w, bar, kb * C::BK, n0);
+        }
+      }
+      // the even CTA's ring barriers count both CTAs' bytes: the newest fills
+      // land before the shared memory goes away
+      if (leader) {
+        const uint32_t first = it > static_cast<uint32_t>(STAGES) ? it - STAGES : 0u;
+        for (uint32_t j = first; j < it; ++j) mbar_wait_drain(smem_u32(&full[j % STAGES]), (j / STAGES) & 1);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (even CTA)
+    if (leader && lane == 0) {
+      constexpr uint32_t kIdesc = idesc_e4m3(256, BN);
+      uint32_t it = 0, tcount = 0;
+      for (int tile = pair; tile < total; tile += pairs, ++tcount) {
+        const uint32_t acc = tcount % C::NUM_ACC;
+        if (!mbar_wait(smem_u32(&acc_empty[acc]), ((tcount / C::NUM_ACC) & 1) ^ 1, abort_flag, p.status)) break;
+        tc_fence_after();
+        const uint32_t d = tmem + acc * BN;
+        bool ok = true;
+        for (int kb = 0; kb < nkb; ++kb, ++it) {
+          const int s = it % STAGES;
+          if (!mbar_wait(smem_u32(&full[s]), (it / STAGES) & 1, abort_flag, p.status)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t a_base = smem_u32(smem + s * C::STAGE_BYTES), w_base = a_base + C::A_BYTES;
+#pragma unroll
+          for (int j = 0; j < C::BK / 32; ++j)
+            mma_e4m3_pair(d, smem_desc(a_base + 32 * j, 16, 1024, kSwizzle128B),
+                          smem_desc(w_base + 32 * j, 16, 1024, kSwizzle128B), kIdesc, (kb > 0 || j > 0) ? 1u : 0u);
+          tc_commit_pair_mc(smem_u32(&empty[s]), 0x3);
+        }
+        if (!ok) break;
+        tc_commit_pair_mc(smem_u32(&acc_full[acc]), 0x3);
+      }
+      tc_commit_pair(smem_u32(drain));
+      mbar_wait_drain(smem_u32(drain), 0);
+    }
+  } else if (warp >= C::EPI_WARP0) {
+    // ------------------------------------------------------------ epilogue (both CTAs)
+    const int ew = warp - C::EPI_WARP0;
+    const int q = warp & 3;    // TMEM lane quarter: rows 32q .. 32q+31 of this CTA
+    const int h = ew >> 2;     // column half
+    const uint32_t acc_empty0 = mapa_shared(smem_u32(&acc_empty[0]), 0);
+    uint8_t* boxes = epi_smem + ew * C::BOXES * C::BOX_BYTES;
+    const uint32_t res_bar = smem_u32(&res_full[ew]);
+    uint32_t loads = 0, used = 0;  // residual fills asked for and waited for
+    auto load_residual = [&](int tile) {
+      const int row0 = (tile % m_tiles) * 2 * C::BM + static_cast<int>(rank) * C::BM + q * 32;
+      const int n0 = (tile / m_tiles) * BN + h * C::HALF;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(res_bar, C::BOXES * C::BOX_BYTES);
+#pragma unroll
+        for (int c = 0; c < C::BOXES; ++c)
+          tma_load_2d(smem_u32(boxes + c * C::BOX_BYTES), &tm_r, res_bar, n0 + 32 * c, row0);
+      }
+      ++loads;
+    };
+    if (p.R != nullptr && pair < total) load_residual(pair);
+    uint32_t tcount = 0;
+    for (int tile = pair; tile < total; tile += pairs, ++tcount) {
+      const int row0 = (tile % m_tiles) * 2 * C::BM + static_cast<int>(rank) * C::BM + q * 32;
+      const int n0 = (tile / m_tiles) * BN + h * C::HALF;
+      const uint32_t acc = tcount % C::NUM_ACC;
+      // (rows past M read the last row's scale; the store drops their outputs)
+      const float sa = __ldg(p.s_a + static_cast<int64_t>(min(row0 + lane, p.M - 1)) * p.s_a_step);
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&acc_full[acc]), (tcount / C::NUM_ACC) & 1, abort_flag,
+                                             p.status)))
+        break;
+      tc_fence_after();
+      if (p.R != nullptr) {
+        if (!__all_sync(0xffffffffu, mbar_wait(res_bar, used & 1, abort_flag, p.status))) break;
+        ++used;
+      } else if (tcount > 0) {
+        // the previous tile's stores have read their boxes
+        if (lane == 0) bulk_wait_group_read<0>();
+        __syncwarp();
+      }
+      const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * BN + h * C::HALF;
+#pragma unroll 1
+      for (int c = 0; c < C::BOXES; ++c) {
+        uint32_t r[32];
+        tmem_ld_32cols(taddr + 32 * c, r);
+        tmem_ld_wait();
+        if (c == C::BOXES - 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(acc_empty0 + 8 * acc);
+        }
+        uint8_t* box = boxes + c * C::BOX_BYTES;
+        const int n = n0 + 32 * c;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int col = n + 8 * g;
+          uint4* slot = reinterpret_cast<uint4*>(box + lane * 64 + ((g ^ ((lane >> 1) & 3)) << 4));
+          float sw[8], y[8];
+          if (col < p.N) {  // N % 8 == 0: all eight columns are valid
+            const float4 w0 = __ldg(reinterpret_cast<const float4*>(p.s_w + col));
+            const float4 w1 = __ldg(reinterpret_cast<const float4*>(p.s_w + col) + 1);
+            sw[0] = w0.x; sw[1] = w0.y; sw[2] = w0.z; sw[3] = w0.w;
+            sw[4] = w1.x; sw[5] = w1.y; sw[6] = w1.z; sw[7] = w1.w;
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sw[j] = 0.0f;
+          }
+          uint32_t b[4] = {0u, 0u, 0u, 0u};
+          if (p.bias != nullptr && col < p.N) {
+            const uint4 bw = __ldg(reinterpret_cast<const uint4*>(p.bias + col));
+            b[0] = bw.x; b[1] = bw.y; b[2] = bw.z; b[3] = bw.w;
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float bj = (j & 1) ? bf16_hi(b[j >> 1]) : bf16_lo(b[j >> 1]);
+            y[j] = fmaf(__uint_as_float(r[8 * g + j]) * sa, sw[j], bj);
+          }
+          if (p.epi == 1) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = gelu_tanh_f32(y[j]);
+          }
+          if (p.R != nullptr) {
+            const uint4 rr = *slot;
+            const uint32_t rs[4] = {rr.x, rr.y, rr.z, rr.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              y[2 * j] += bf16_lo(rs[j]);
+              y[2 * j + 1] += bf16_hi(rs[j]);
+            }
+          }
+          *slot = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
+                             pack_bf16x2(y[6], y[7]));
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_2d(&tm_y, smem_u32(box), n, row0);
+          bulk_commit_group();
+        }
+      }
+      if (p.R != nullptr && tile + pairs < total) {
+        if (lane == 0) bulk_wait_group_read<0>();
+        __syncwarp();
+        load_residual(tile + pairs);
+      }
+    }
+    // no residual fill may still be landing, no store still be reading
+    if (lane == 0) {
+      for (; used < loads; ++used) mbar_wait_drain(res_bar, used & 1);
+      bulk_wait_group_all();
+    }
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  cluster_sync();  // no CTA leaves while its peer may still signal it or read its TMEM
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, C::TMEM_COLS);
+  }
+}
+
+// ------------------------------------------------------------------ few rows
+// At most TN tokens: the weight is read once and nothing else matters, so its
+// rows are the MMA's 128-row operand and the tokens its N.  A CTA takes 128
+// weight rows and one of gridDim.y / cluster-many slices of K, streams them
+// through a TMA ring (two CTAs an SM keep about 180 KB in flight), and leaves
+// its fp32 sums [token][weight row] in shared memory; after a cluster barrier
+// every CTA of the cluster adds up its share of the tokens over the slices, in
+// slice order, and writes them.  128 threads: warp 0 TMA producer and TMEM
+// owner, warp 1 MMA issuer, all four warps the epilogue (one weight row a
+// thread).
+template <int TN_, int STAGES_>
+struct Fp8SmallCfg {
+  static constexpr int TN = TN_, STAGES = STAGES_, BM = 128, BK = 128;
+  static constexpr int W_BYTES = BM * BK, X_BYTES = TN * BK, STAGE_BYTES = W_BYTES + X_BYTES;
+  static constexpr int TMEM_COLS = TN < 32 ? 32 : TN;
+  static constexpr int THREADS = 128;
+  static constexpr int PART_BYTES = TN * BM * 4;  // reuses the ring
+  static constexpr int RING_BYTES = STAGES * STAGE_BYTES;
+  static constexpr int BAR_BYTES = (8 * (2 * STAGES + 1) + 8 + 127) / 128 * 128;
+  static constexpr int SMEM = RING_BYTES + BAR_BYTES + 1024;
+  static_assert(PART_BYTES <= RING_BYTES, "the partial sums fit the ring");
+  static_assert(STAGE_BYTES % 1024 == 0 && SMEM <= 113 * 1024, "two CTAs per SM");
+};
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, 2)
+    gemm_fp8_small_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
+                          const Fp8GemmParams p) {
+  constexpr int STAGES = C::STAGES;
+  grid_launch_dependents();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::RING_BYTES);
+  uint64_t* empty = full + STAGES;
+  uint64_t* done = empty + STAGES;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int splits = gridDim.x;               // the cluster spans the K slices of one weight tile
+  const int split = blockIdx.x;
+  const int n0 = blockIdx.y * C::BM;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), 1);
+    }
+    mbar_init(smem_u32(done), 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tm_w);
+    tma_prefetch_desc(&tm_x);
+  }
+  if (warp == 0) {
+    tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  grid_dependency_wait();
+
+  // K steps [k0, k1): the slices differ by one step at most (the launch never
+  // has more slices than steps)
+  const int nkb = (p.K + C::BK - 1) / C::BK;
+  const int k0 = static_cast<int>(static_cast<int64_t>(nkb) * split / splits);
+  const int k1 = static_cast<int>(static_cast<int64_t>(nkb) * (split + 1) / splits);
+  const int steps = k1 - k0;
+  if (warp == 0 && lane == 0) {
+    int it = 0;
+    for (; it < steps; ++it) {
+      const int s = it % STAGES;
+      if (!mbar_wait(smem_u32(&empty[s]), ((it / STAGES) & 1) ^ 1, abort_flag, p.status)) break;
+      uint8_t* st = smem + s * C::STAGE_BYTES;
+      const uint32_t bar = smem_u32(&full[s]);
+      mbar_arrive_expect_tx(bar, C::STAGE_BYTES);
+      tma_load_2d(smem_u32(st), &tm_w, bar, (k0 + it) * C::BK, n0);
+      tma_load_2d(smem_u32(st + C::W_BYTES), &tm_x, bar, (k0 + it) * C::BK, 0);
+    }
+    for (int j = max(0, it - STAGES); j < it; ++j) mbar_wait_drain(smem_u32(&full[j % STAGES]), (j / STAGES) & 1);
+  } else if (warp == 1 && lane == 0) {
+    constexpr uint32_t kIdesc = idesc_e4m3(C::BM, C::TN);
+    for (int it = 0; it < steps; ++it) {
+      const int s = it % STAGES;
+      if (!mbar_wait(smem_u32(&full[s]), (it / STAGES) & 1, abort_flag, p.status)) break;
+      tc_fence_after();
+      const uint32_t w_base = smem_u32(smem + s * C::STAGE_BYTES), x_base = w_base + C::W_BYTES;
+#pragma unroll
+      for (int j = 0; j < C::BK / 32; ++j)
+        mma_e4m3(tmem, smem_desc(w_base + 32 * j, 16, 1024, kSwizzle128B),
+                 smem_desc(x_base + 32 * j, 16, 1024, kSwizzle128B), kIdesc, (it > 0 || j > 0) ? 1u : 0u);
+      tc_commit(smem_u32(&empty[s]));
+    }
+    tc_commit(smem_u32(done));  // completes once every MMA above has, abort or not
+  }
+  __syncwarp();
+  const bool ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(done), 0, abort_flag, p.status));
+  if (!ok) mbar_wait_drain(smem_u32(done), 0);
+  tc_fence_after();
+  // every fill has landed and been read: the ring now holds the partial sums
+  __syncthreads();
+  float* part = reinterpret_cast<float*>(smem);  // [token][128 weight rows]
+  const int row = threadIdx.x;                    // weight row of the tile, and TMEM lane
+#pragma unroll 1
+  for (int c = 0; c < C::TN && c < p.M; c += 16) {
+    uint32_t r[16];
+    tmem_ld_16cols(tmem + (static_cast<uint32_t>(warp * 32) << 16) + c, r);
+    tmem_ld_wait();
+#pragma unroll
+    for (int j = 0; j < 16; ++j) part[(c + j) * C::BM + row] = ok ? __uint_as_float(r[j]) : 0.0f;
+  }
+  cluster_sync();
+  const int n = n0 + row;
+  if (ok && n < p.N) {
+    const float sw = __ldg(p.s_w + n);
+    const float b = p.bias != nullptr ? __bfloat162float(p.bias[n]) : 0.0f;
+    const uint32_t mine = smem_u32(part + row);
+    for (int m = split; m < p.M; m += splits) {
+      float acc = 0.0f;
+      for (int s = 0; s < splits; ++s) {
+        float v;
+        asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                     : "=f"(v)
+                     : "r"(mapa_shared(mine + static_cast<uint32_t>(m) * C::BM * 4, static_cast<uint32_t>(s)))
+                     : "memory");
+        acc += v;
+      }
+      float y = fmaf(acc * __ldg(p.s_a + static_cast<int64_t>(m) * p.s_a_step), sw, b);
+      if (p.epi == 1) y = gelu_tanh_f32(y);
+      if (p.R != nullptr) y += __bfloat162float(p.R[static_cast<int64_t>(m) * p.ldr + n]);
+      p.Y[static_cast<int64_t>(m) * p.ldy + n] = __float2bfloat16_rn(y);
+    }
+  }
+  tc_fence_before();
+  cluster_sync();  // the peers have read this CTA's partial sums
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+}  // namespace w4a4

@@ -1,0 +1,192 @@
+// rows_fp8.cuh -- E4M3 codes with one fp32 scale per row: of a tensor as it
+// stands, or of its root-mean-square norm after the residual's addition.
+//
+// Per row m of D columns, in fp32 and rounded once at each output:
+//   h = x + r                      (r optional; hidden = bf16(h) optional)
+//   v = h * w                      (w optional)
+//   i = 1 / sqrt(sum(h^2) / D + eps)   (1 without the norm)
+//   s = i * max|v| / 448           (1 when that is not a normal number)
+//   code = E4M3_rn_satfinite(v * (i * (1 / s)))
+//   normed = bf16(v * i)           (optional)
+// The factor i is common to the row, so the sum of squares and max|v| come
+// from one pass and one reduction, and the row stays in registers: every
+// input is read once and every output written once.  That traffic (for
+// x, r, hidden and codes 7 bytes an element) is the bound.
+//
+// Two shapes: rows of up to 1024 columns take a power of two of lanes of one
+// warp (shuffles only); wider ones a block of their own, a thread holding V
+// 16-byte vectors of the row.
+#pragma once
+
+#include "sm100.cuh"
+
+namespace w4a4 {
+
+constexpr int kRowsMaxCols = 32768;    // 1024 threads of four vectors of eight
+constexpr int kRowsWarpCols = 1024;    // one warp, four vectors a lane
+constexpr int kRowsWarpThreads = 256;  // block size of the warp-per-row shape
+
+struct RowsFp8Params {
+  const __nv_bfloat16* x;
+  const __nv_bfloat16* r;   // or nullptr
+  const __nv_bfloat16* w;   // or nullptr
+  __nv_bfloat16* hidden;    // or nullptr; may be x or r itself
+  __nv_bfloat16* normed;    // or nullptr
+  uint8_t* codes;           // or nullptr (then scales is unused)
+  float* scales;
+  int64_t rows, ldx, ldr, ldh, ldn, ldo;
+  int cols;
+  float eps;
+};
+
+struct RowStats {
+  float sum, top;  // sum of h^2, max |v|
+};
+
+// This thread's vectors t0, t0 + step, ... of the row: loads, hidden, v and
+// the partial statistics.
+template <int V, bool NORM>
+__device__ __forceinline__ RowStats rows_load(const RowsFp8Params& p, int64_t row, int t0, int step,
+                                              float (&v)[8 * V]) {
+  const int nv = p.cols >> 3;
+  uint4 xw[V], rw[V];
+  const uint4* xr = reinterpret_cast<const uint4*>(p.x + row * p.ldx);
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int t = t0 + i * step;
+    xw[i] = t < nv ? xr[t] : make_uint4(0u, 0u, 0u, 0u);
+  }
+  if (NORM && p.r != nullptr) {
+    const uint4* rr = reinterpret_cast<const uint4*>(p.r + row * p.ldr);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int t = t0 + i * step;
+      rw[i] = t < nv ? rr[t] : make_uint4(0u, 0u, 0u, 0u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) rw[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  RowStats st = {0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const uint32_t xs[4] = {xw[i].x, xw[i].y, xw[i].z, xw[i].w};
+    const uint32_t rs[4] = {rw[i].x, rw[i].y, rw[i].z, rw[i].w};
+    float* vi = v + 8 * i;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      vi[2 * j] = bf16_lo(xs[j]);
+      vi[2 * j + 1] = bf16_hi(xs[j]);
+      if (NORM && p.r != nullptr) {
+        vi[2 * j] += bf16_lo(rs[j]);
+        vi[2 * j + 1] += bf16_hi(rs[j]);
+      }
+    }
+    const int t = t0 + i * step;
+    if (NORM) {
+      if (p.hidden != nullptr && t < nv)
+        reinterpret_cast<uint4*>(p.hidden + row * p.ldh)[t] =
+            make_uint4(pack_bf16x2(vi[0], vi[1]), pack_bf16x2(vi[2], vi[3]), pack_bf16x2(vi[4], vi[5]),
+                       pack_bf16x2(vi[6], vi[7]));
+#pragma unroll
+      for (int j = 0; j < 8; ++j) st.sum = fmaf(vi[j], vi[j], st.sum);
+      if (p.w != nullptr && t < nv) {
+        const uint4 ww = __ldg(reinterpret_cast<const uint4*>(p.w) + t);
+        const uint32_t wsv[4] = {ww.x, ww.y, ww.z, ww.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          vi[2 * j] *= bf16_lo(wsv[j]);
+          vi[2 * j + 1] *= bf16_hi(wsv[j]);
+        }
+      }
+    }
+    st.top = fmaxf(st.top, fmaxf(fmaxf(fmaxf(fabsf(vi[0]), fabsf(vi[1])), fmaxf(fabsf(vi[2]), fabsf(vi[3]))),
+                                 fmaxf(fmaxf(fabsf(vi[4]), fabsf(vi[5])), fmaxf(fabsf(vi[6]), fabsf(vi[7])))));
+  }
+  return st;
+}
+
+// The row's factor and scale, then this thread's outputs.
+template <int V, bool NORM>
+__device__ __forceinline__ void rows_store(const RowsFp8Params& p, int64_t row, int t0, int step, bool first,
+                                           RowStats st, const float (&v)[8 * V]) {
+  const int nv = p.cols >> 3;
+  const float inv = NORM ? 1.0f / sqrtf(st.sum / static_cast<float>(p.cols) + p.eps) : 1.0f;
+  if (p.codes != nullptr) {
+    float s = (NORM ? st.top * inv : st.top) / 448.0f;
+    if (!(s >= 1.17549435e-38f && s < INFINITY)) s = 1.0f;
+    if (first) p.scales[row] = s;
+    const float f = NORM ? inv * (1.0f / s) : 1.0f / s;
+    uint2* out = reinterpret_cast<uint2*>(p.codes + row * p.ldo);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int t = t0 + i * step;
+      const float* vi = v + 8 * i;
+      if (t < nv)
+        out[t] = make_uint2(cvt_e4m3x2(vi[1] * f, vi[0] * f) | (cvt_e4m3x2(vi[3] * f, vi[2] * f) << 16),
+                            cvt_e4m3x2(vi[5] * f, vi[4] * f) | (cvt_e4m3x2(vi[7] * f, vi[6] * f) << 16));
+    }
+  }
+  if (NORM && p.normed != nullptr) {
+    uint4* out = reinterpret_cast<uint4*>(p.normed + row * p.ldn);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int t = t0 + i * step;
+      const float* vi = v + 8 * i;
+      if (t < nv)
+        out[t] = make_uint4(pack_bf16x2(vi[0] * inv, vi[1] * inv), pack_bf16x2(vi[2] * inv, vi[3] * inv),
+                            pack_bf16x2(vi[4] * inv, vi[5] * inv), pack_bf16x2(vi[6] * inv, vi[7] * inv));
+    }
+  }
+}
+
+// A row per `lanes` lanes (a power of two up to 32) of a warp.
+template <int V, bool NORM>
+__global__ void __launch_bounds__(kRowsWarpThreads) rows_fp8_warp_kernel(const RowsFp8Params p, int lanes) {
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int per_block = kRowsWarpThreads / lanes;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * per_block + threadIdx.x / lanes;
+  const int t0 = threadIdx.x & (lanes - 1);
+  const bool live = row < p.rows;  // the shuffles below take whole warps
+  float v[8 * V];
+  RowStats st = {0.0f, 0.0f};
+  if (live) st = rows_load<V, NORM>(p, row, t0, lanes, v);
+  for (int o = lanes >> 1; o > 0; o >>= 1) {
+    if (NORM) st.sum += __shfl_xor_sync(0xffffffffu, st.sum, o);
+    st.top = fmaxf(st.top, __shfl_xor_sync(0xffffffffu, st.top, o));
+  }
+  if (live) rows_store<V, NORM>(p, row, t0, lanes, t0 == 0, st, v);
+}
+
+// A row per block.
+template <int V, bool NORM>
+__global__ void __launch_bounds__(1024) rows_fp8_block_kernel(const RowsFp8Params p) {
+  __shared__ float red_sum[32], red_top[32];
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int64_t row = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  float v[8 * V];
+  RowStats st = rows_load<V, NORM>(p, row, threadIdx.x, blockDim.x, v);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    if (NORM) st.sum += __shfl_xor_sync(0xffffffffu, st.sum, o);
+    st.top = fmaxf(st.top, __shfl_xor_sync(0xffffffffu, st.top, o));
+  }
+  if (lane == 0) {
+    if (NORM) red_sum[warp] = st.sum;
+    red_top[warp] = st.top;
+  }
+  __syncthreads();
+  st.sum = NORM && lane < warps ? red_sum[lane] : 0.0f;
+  st.top = lane < warps ? red_top[lane] : 0.0f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    if (NORM) st.sum += __shfl_xor_sync(0xffffffffu, st.sum, o);
+    st.top = fmaxf(st.top, __shfl_xor_sync(0xffffffffu, st.top, o));
+  }
+  rows_store<V, NORM>(p, row, threadIdx.x, blockDim.x, threadIdx.x == 0, st, v);
+}
+
+}  // namespace w4a4

@@ -18,7 +18,10 @@
 
 #include "quant.cuh"
 #include "attention.cuh"
+#include "cross_attention.cuh"
+#include "gemm_fp8.cuh"
 #include "mma_rate.cuh"
+#include "rows_fp8.cuh"
 
 namespace w4a4 {
 
@@ -49,9 +52,24 @@ using PairQNext = Gemm2Cfg<256, 6, 3, 1, false, true>;
 // ... and the one whose epilogue can apply the rotary embedding
 using PairRope = Gemm2Cfg<256, 6, 3, 1, false, false, true>;
 
+// FP8 linear layer: pair tiles 256, 128 and 64 columns wide, and the kernel
+// for few rows at 16, 32, 64 and 128 tokens.
+using Fp8Pair256 = Fp8PairCfg<256, 5>;
+using Fp8Pair128 = Fp8PairCfg<128, 7>;
+using Fp8Pair64 = Fp8PairCfg<64, 8>;
+using Fp8Small16 = Fp8SmallCfg<16, 6>;
+using Fp8Small32 = Fp8SmallCfg<32, 5>;
+using Fp8Small64 = Fp8SmallCfg<64, 4>;
+using Fp8Small128 = Fp8SmallCfg<128, 3>;
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t round256(size_t v) { return (v + 255) & ~size_t(255); }
+
+template <class C, class Kernel>
+bool smem_attr(Kernel* kernel) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) == cudaSuccess;
+}
 
 // Per-device set-up: architecture check, SM count, kernel attributes, the
 // device address of the status word.  Returns W4A4_OK or an error.
@@ -116,6 +134,18 @@ int device_setup(DeviceInfo** out) {
                                   PairQNext::SMEM) == cudaSuccess;
   attr_ok &= cudaFuncSetAttribute(gemm2_kernel<PairRope>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   PairRope::SMEM) == cudaSuccess;
+
+  attr_ok &= smem_attr<Fp8Pair256>(gemm_fp8_pair_kernel<Fp8Pair256>) &&
+             smem_attr<Fp8Pair128>(gemm_fp8_pair_kernel<Fp8Pair128>) &&
+             smem_attr<Fp8Pair64>(gemm_fp8_pair_kernel<Fp8Pair64>);
+  attr_ok &= smem_attr<Fp8Small16>(gemm_fp8_small_kernel<Fp8Small16>) &&
+             smem_attr<Fp8Small32>(gemm_fp8_small_kernel<Fp8Small32>) &&
+             smem_attr<Fp8Small64>(gemm_fp8_small_kernel<Fp8Small64>) &&
+             smem_attr<Fp8Small128>(gemm_fp8_small_kernel<Fp8Small128>);
+  attr_ok &= smem_attr<XAttnCfg<1, false>>(cross_attention_kernel<XAttnCfg<1, false>>) &&
+             smem_attr<XAttnCfg<2, false>>(cross_attention_kernel<XAttnCfg<2, false>>) &&
+             smem_attr<XAttnCfg<1, true>>(cross_attention_kernel<XAttnCfg<1, true>>) &&
+             smem_attr<XAttnCfg<2, true>>(cross_attention_kernel<XAttnCfg<2, true>>);
 
   if (!attr_ok) { cudaGetLastError(); return W4A4_ERR_CUDA; }
   d.ok = true;
@@ -258,6 +288,7 @@ QuantPlan quant_plan(int64_t M, int64_t K, int r) {
 // (weight) or 2^21 bf16 columns.  One bound for every entry point.
 constexpr int64_t kMaxK = int64_t(kAmaxMaxBlocks) * kAmaxThreads * 4;
 static_assert(kMaxK == (int64_t(1) << 20) && kMaxK == W4A4_MAX_K, "K bound of the header");
+static_assert(kRowsMaxCols == W4A4_MAX_ROW_COLS, "row bound of the header");
 // Largest column count of fp8_quantize (bf16 only: eight per segment).
 constexpr int64_t kFp8MaxCols = int64_t(kAmaxMaxBlocks) * kAmaxThreads * 8;
 
@@ -629,6 +660,198 @@ int launch_gemm_pair(const uint8_t* Xq, const uint8_t* Xsf, const float* t_x, co
   return W4A4_OK;
 }
 
+// ------------------------------------------------------------------ row codes, RMS norm
+template <bool NORM>
+int launch_rows_fp8(const RowsFp8Params& p, cudaStream_t stream) {
+  const int nv = p.cols / 8;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // set-up overlaps the previous kernel
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e;
+  if (p.cols <= kRowsWarpCols) {
+    int lanes = 1;
+    while (lanes < 32 && lanes < nv) lanes *= 2;
+    const int64_t per_block = kRowsWarpThreads / lanes;
+    cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(p.rows, per_block)), 1, 1);
+    cfg.blockDim = dim3(kRowsWarpThreads, 1, 1);
+    e = nv <= 32   ? cudaLaunchKernelEx(&cfg, rows_fp8_warp_kernel<1, NORM>, p, lanes)
+        : nv <= 64 ? cudaLaunchKernelEx(&cfg, rows_fp8_warp_kernel<2, NORM>, p, lanes)
+                   : cudaLaunchKernelEx(&cfg, rows_fp8_warp_kernel<4, NORM>, p, lanes);
+  } else {
+    const int vecs = nv <= 512 ? 1 : nv <= 2048 ? 2 : 4;
+    cfg.gridDim = dim3(static_cast<unsigned>(p.rows), 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(ceil_div(ceil_div(nv, vecs), 32) * 32), 1, 1);
+    e = vecs == 1   ? cudaLaunchKernelEx(&cfg, rows_fp8_block_kernel<1, NORM>, p)
+        : vecs == 2 ? cudaLaunchKernelEx(&cfg, rows_fp8_block_kernel<2, NORM>, p)
+                    : cudaLaunchKernelEx(&cfg, rows_fp8_block_kernel<4, NORM>, p);
+  }
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return W4A4_ERR_CUDA;
+  }
+  return W4A4_OK;
+}
+
+// ------------------------------------------------------------------ FP8 linear layer
+template <class C>
+int launch_fp8_pair(const uint8_t* A8, int64_t lda, const uint8_t* W8, int64_t ldw, const Fp8GemmParams& p,
+                    cudaStream_t stream, DeviceInfo* dev) {
+  CUtensorMap ta, tw, tr, ty;
+  const uint64_t M = static_cast<uint64_t>(p.M), N = static_cast<uint64_t>(p.N), K = static_cast<uint64_t>(p.K);
+  if (!encode_2d(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, A8, K, M, static_cast<uint64_t>(lda), 128u, 128u,
+                 CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, W8, K, N, static_cast<uint64_t>(ldw), 128u,
+                 static_cast<uint32_t>(C::BH), CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_2d(&ty, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.Y, N, M, static_cast<uint64_t>(p.ldy) * 2, 32u, 32u,
+                 CU_TENSOR_MAP_SWIZZLE_64B))
+    return W4A4_ERR_CUDA;
+  tr = ty;  // unused without a residual
+  if (p.R != nullptr && !encode_2d(&tr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.R, N, M,
+                                   static_cast<uint64_t>(p.ldr) * 2, 32u, 32u, CU_TENSOR_MAP_SWIZZLE_64B))
+    return W4A4_ERR_CUDA;
+  const int64_t tiles = ceil_div(p.M, 2 * C::BM) * ceil_div(p.N, C::BN);
+  const int64_t pairs = std::min<int64_t>(tiles, dev->num_sms / 2);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs), 1, 1);
+  cfg.blockDim = dim3(C::THREADS, 1, 1);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // set-up overlaps the previous kernel
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, gemm_fp8_pair_kernel<C>, ta, tw, tr, ty, p) != cudaSuccess) {
+    cudaGetLastError();
+    return W4A4_ERR_CUDA;
+  }
+  return W4A4_OK;
+}
+
+// K slices of the kernel for few rows: a power of two up to a cluster of
+// eight, at most one per 128-deep step, while the CTAs still fit on the device
+// at once (two per SM).
+int fp8_small_splits(int64_t n_tiles, int64_t k_steps, int64_t sms) {
+  int s = 1;
+  while (s < 8 && 2 * s <= k_steps && n_tiles * 2 * s <= 2 * sms) s *= 2;
+  return s;
+}
+
+template <class C>
+int launch_fp8_small(const uint8_t* A8, int64_t lda, const uint8_t* W8, int64_t ldw, const Fp8GemmParams& p,
+                     cudaStream_t stream, DeviceInfo* dev) {
+  CUtensorMap tw, tx;
+  const uint64_t M = static_cast<uint64_t>(p.M), N = static_cast<uint64_t>(p.N), K = static_cast<uint64_t>(p.K);
+  if (!encode_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, W8, K, N, static_cast<uint64_t>(ldw), 128u, 128u,
+                 CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_UINT8, A8, K, M, static_cast<uint64_t>(lda), 128u,
+                 static_cast<uint32_t>(C::TN), CU_TENSOR_MAP_SWIZZLE_128B))
+    return W4A4_ERR_CUDA;
+  const int64_t tiles = ceil_div(p.N, C::BM);
+  const int splits = fp8_small_splits(tiles, ceil_div(p.K, C::BK), dev->num_sms);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(splits), static_cast<unsigned>(tiles), 1);
+  cfg.blockDim = dim3(C::THREADS, 1, 1);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(splits);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // set-up overlaps the previous kernel
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, gemm_fp8_small_kernel<C>, tw, tx, p) != cudaSuccess) {
+    cudaGetLastError();
+    return W4A4_ERR_CUDA;
+  }
+  return W4A4_OK;
+}
+
+// ------------------------------------------------------------------ cross attention
+// A head-wise view [batch, S, heads, D] of token-major rows: box of 64
+// columns x `heads_box` heads x `tokens_box` tokens.
+bool encode_heads(CUtensorMap* m, const void* ptr, int64_t D, int64_t heads, int64_t S, int64_t batch, int64_t ld,
+                  uint32_t heads_box, uint32_t tokens_box) {
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(S),
+                              static_cast<cuuint64_t>(batch)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(ld) * 2,
+                                 static_cast<cuuint64_t>(S) * static_cast<cuuint64_t>(ld) * 2};
+  const cuuint32_t box[4] = {64, heads_box, tokens_box, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Which form a problem takes: splits == 0 the persistent one (256 rows a work
+// tile), else the split one (128 rows) with that many CTAs of a cluster on the
+// keys of a tile.  Both are costed in key tiles run one after another.
+struct XPlan {
+  int splits = 0;
+};
+
+XPlan xattn_plan(int64_t rows, int64_t head_blocks, int64_t key_tiles, int64_t sms) {
+  XPlan best;
+  // persistent: two row tiles against a key tile at a time, about 2.2 units
+  // (a unit: one softmax stream's tile in the split form), 2 to begin and end
+  int64_t cost = ceil_div(ceil_div(rows, 2 * kXTile) * head_blocks, sms) * (22 * key_tiles + 20);
+  const int64_t units = ceil_div(rows, kXTile) * head_blocks;
+  if (units > 65535) return best;
+  for (int s = 1; s <= 8 && s <= key_tiles; s *= 2) {
+    const int64_t c = ceil_div(units * s, sms) * (12 * ceil_div(key_tiles, s) + 25 + 5 * (s > 1));
+    if (c < cost) {
+      cost = c;
+      best.splits = s;
+    }
+  }
+  return best;
+}
+
+template <class C>
+int launch_cross_attention(const void* Q, int64_t ldq, const void* K, int64_t ldk, const void* V, int64_t ldv,
+                           XAttnParams p, int splits, cudaStream_t stream, DeviceInfo* dev) {
+  CUtensorMap tq, tk, tv, to;
+  const uint32_t pack = static_cast<uint32_t>(p.pack);
+  if (!encode_heads(&tq, Q, p.D, p.heads, p.Sq, p.batch, ldq, pack, kXTile / pack) ||
+      !encode_heads(&tk, K, p.D, p.kv_heads, p.Skv, p.kv_batch, ldk, 1, kXTile) ||
+      !encode_heads(&tv, V, p.D, p.kv_heads, p.Skv, p.kv_batch, ldv, 1, kXTile) ||
+      !encode_heads(&to, p.O, p.D, p.heads, p.Sq, p.batch, p.ldo, pack, 32 / pack))
+    return W4A4_ERR_CUDA;
+  p.row_tiles = static_cast<int>(ceil_div(static_cast<int64_t>(p.Sq) * p.pack, C::SPLIT ? kXTile : 2 * kXTile));
+  p.tiles = p.row_tiles * (p.heads / p.pack) * p.batch;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = C::SPLIT ? dim3(static_cast<unsigned>(splits), static_cast<unsigned>(p.tiles), 1)
+                         : dim3(static_cast<unsigned>(std::min(p.tiles, dev->num_sms)), 1, 1);
+  cfg.blockDim = dim3(kXThreads, 1, 1);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // set-up overlaps the previous kernel
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(splits);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = C::SPLIT ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, cross_attention_kernel<C>, tq, tk, tv, to, p) != cudaSuccess) {
+    cudaGetLastError();
+    return W4A4_ERR_CUDA;
+  }
+  return W4A4_OK;
+}
+
 int check_gemm_args(const uint8_t* Xq, const uint8_t* Xsf, const float* t_x, const void* U, int64_t M, int64_t N,
                     int64_t K, const uint8_t* Wq, const uint8_t* Wsf, const float* t_w, const void* L2t, int r,
                     const void* bias, int epi, const void* Y, int64_t ldy) {
@@ -982,6 +1205,177 @@ int attention_fp8(const uint8_t* Q8, const uint8_t* K8, const uint8_t* Vt8, int6
     return W4A4_ERR_CUDA;
   }
   return W4A4_OK;
+}
+
+static int rows_fp8_args(int64_t rows, int64_t cols, const void* X, int64_t ldx, const uint8_t* codes, int64_t ldo,
+                         const float* scales) {
+  if (rows < 0 || rows > (int64_t(1) << 30) || cols <= 0 || cols % 8 != 0 || cols > W4A4_MAX_ROW_COLS || ldx < cols ||
+      ldx % 8 != 0 || (codes && (ldo < cols || ldo % 8 != 0)))
+    return W4A4_ERR_SHAPE;
+  if (rows == 0) return W4A4_OK;
+  if (!X || (codes && !scales)) return W4A4_ERR_NULL;
+  if (!aligned16(X) || !aligned16(codes) || reinterpret_cast<uintptr_t>(scales) % 4 != 0) return W4A4_ERR_ALIGN;
+  return W4A4_OK;
+}
+
+int fp8_quantize_rows(const void* X, int64_t rows, int64_t cols, int64_t ldx, uint8_t* codes, int64_t ldo,
+                      float* scales, void* stream) {
+  if (rows > 0 && !codes) return W4A4_ERR_NULL;
+  int st = rows_fp8_args(rows, cols, X, ldx, codes, ldo, scales);
+  if (st != W4A4_OK || rows == 0) return st;
+  DeviceInfo* dev = nullptr;
+  st = device_setup(&dev);
+  if (st != W4A4_OK) return st;
+  RowsFp8Params p = {};
+  p.x = static_cast<const __nv_bfloat16*>(X);
+  p.codes = codes;
+  p.scales = scales;
+  p.rows = rows;
+  p.cols = static_cast<int>(cols);
+  p.ldx = ldx;
+  p.ldo = ldo;
+  return launch_rows_fp8<false>(p, static_cast<cudaStream_t>(stream));
+}
+
+int rmsnorm_fp8(const void* X, int64_t rows, int64_t cols, int64_t ldx, const void* R, int64_t ldr, const void* weight,
+                float eps, void* hidden, int64_t ldh, void* normed, int64_t ldn, uint8_t* codes, int64_t ldo,
+                float* scales, void* stream) {
+  int st = rows_fp8_args(rows, cols, X, ldx, codes, ldo, scales);
+  if (st != W4A4_OK) return st;
+  if ((R && (ldr < cols || ldr % 8 != 0)) || (hidden && (ldh < cols || ldh % 8 != 0)) ||
+      (normed && (ldn < cols || ldn % 8 != 0)))
+    return W4A4_ERR_SHAPE;
+  if (!(eps >= 0.0f) || !(eps < 3.0e38f)) return W4A4_ERR_ARG;
+  if (rows == 0) return W4A4_OK;
+  if (!codes && !normed) return W4A4_ERR_NULL;
+  if (!aligned16(R) || !aligned16(weight) || !aligned16(hidden) || !aligned16(normed)) return W4A4_ERR_ALIGN;
+  DeviceInfo* dev = nullptr;
+  st = device_setup(&dev);
+  if (st != W4A4_OK) return st;
+  RowsFp8Params p = {};
+  p.x = static_cast<const __nv_bfloat16*>(X);
+  p.r = static_cast<const __nv_bfloat16*>(R);
+  p.w = static_cast<const __nv_bfloat16*>(weight);
+  p.hidden = static_cast<__nv_bfloat16*>(hidden);
+  p.normed = static_cast<__nv_bfloat16*>(normed);
+  p.codes = codes;
+  p.scales = scales;
+  p.rows = rows;
+  p.cols = static_cast<int>(cols);
+  p.ldx = ldx;
+  p.ldr = ldr;
+  p.ldh = ldh;
+  p.ldn = ldn;
+  p.ldo = ldo;
+  p.eps = eps;
+  return launch_rows_fp8<true>(p, static_cast<cudaStream_t>(stream));
+}
+
+int fp8_gemm(const uint8_t* A8, int64_t lda, const float* s_a, int s_a_rows, int64_t M, int64_t N, int64_t K,
+             const uint8_t* W8, int64_t ldw, const float* s_w, const void* bias, int epilogue, const void* R,
+             int64_t ldr, void* Y, int64_t ldy, void* stream) {
+  if (M < 0 || N <= 0 || N % 8 != 0 || K <= 0 || K % 16 != 0 || K > kMaxK || M > (int64_t(1) << 30) ||
+      N > (int64_t(1) << 30) || lda < K || lda % 16 != 0 || ldw < K || ldw % 16 != 0 || ldy < N || ldy % 8 != 0 ||
+      (R && (ldr < N || ldr % 8 != 0)) || lda >= (int64_t(1) << 40) || ldw >= (int64_t(1) << 40) ||
+      ldy >= (int64_t(1) << 39) || (R && ldr >= (int64_t(1) << 39)) ||
+      ceil_div(M, 256) * ceil_div(N, 64) > (int64_t(1) << 30))
+    return W4A4_ERR_SHAPE;  // (row pitches fit a tensor map, tile counts 32 bits)
+  if ((s_a_rows != 0 && s_a_rows != 1) || (epilogue != W4A4_EPI_NONE && epilogue != W4A4_EPI_GELU_TANH))
+    return W4A4_ERR_ARG;
+  if (M == 0) return W4A4_OK;
+  if (!A8 || !s_a || !W8 || !s_w || !Y) return W4A4_ERR_NULL;
+  if (!aligned16(A8) || !aligned16(W8) || !aligned16(s_w) || !aligned16(bias) || !aligned16(R) || !aligned16(Y) ||
+      reinterpret_cast<uintptr_t>(s_a) % 4 != 0)
+    return W4A4_ERR_ALIGN;
+  DeviceInfo* dev = nullptr;
+  int st = device_setup(&dev);
+  if (st != W4A4_OK) return st;
+  Fp8GemmParams p;
+  p.M = static_cast<int>(M);
+  p.N = static_cast<int>(N);
+  p.K = static_cast<int>(K);
+  p.s_a = s_a;
+  p.s_a_step = s_a_rows;
+  p.s_w = s_w;
+  p.bias = static_cast<const __nv_bfloat16*>(bias);
+  p.R = static_cast<const __nv_bfloat16*>(R);
+  p.Y = static_cast<__nv_bfloat16*>(Y);
+  p.ldr = ldr;
+  p.ldy = ldy;
+  p.epi = epilogue;
+  p.status = dev->status_ptr;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (M <= 128 && ceil_div(N, 128) <= 65535) {
+    if (M <= 16) return launch_fp8_small<Fp8Small16>(A8, lda, W8, ldw, p, s, dev);
+    if (M <= 32) return launch_fp8_small<Fp8Small32>(A8, lda, W8, ldw, p, s, dev);
+    if (M <= 64) return launch_fp8_small<Fp8Small64>(A8, lda, W8, ldw, p, s, dev);
+    return launch_fp8_small<Fp8Small128>(A8, lda, W8, ldw, p, s, dev);
+  }
+  const int64_t pairs = dev->num_sms / 2, m_tiles = ceil_div(M, 256);
+  if (m_tiles * ceil_div(N, 128) <= pairs) return launch_fp8_pair<Fp8Pair64>(A8, lda, W8, ldw, p, s, dev);
+  if (m_tiles * ceil_div(N, 256) <= pairs) return launch_fp8_pair<Fp8Pair128>(A8, lda, W8, ldw, p, s, dev);
+  return launch_fp8_pair<Fp8Pair256>(A8, lda, W8, ldw, p, s, dev);
+}
+
+int cross_attention_bf16(const void* Q, int64_t ldq, const void* K, int64_t ldk, const void* V, int64_t ldv,
+                         int64_t batch, int64_t kv_batch, int64_t Sq, int64_t Skv, int64_t heads, int64_t kv_heads,
+                         int64_t d_head, const int* kv_len, const uint8_t* key_mask, int64_t ld_mask,
+                         float softmax_scale, void* O, int64_t ldo, void* stream) {
+  if (batch < 0 || Sq < 0 || Skv < 0 || heads <= 0 || kv_heads <= 0 || heads % kv_heads != 0 || heads > 65535 ||
+      batch > 65535 || d_head < 8 || d_head > 128 || d_head % 8 != 0 || Sq > (int64_t(1) << 24) ||
+      Skv > (int64_t(1) << 24) || (kv_batch != 1 && kv_batch != batch))
+    return W4A4_ERR_SHAPE;
+  const int64_t wq = heads * d_head, wk = kv_heads * d_head, ld_max = int64_t(1) << 31;
+  if (ldq < wq || ldq % 8 != 0 || ldk < wk || ldk % 8 != 0 || ldv < wk || ldv % 8 != 0 || ldo < wq || ldo % 8 != 0 ||
+      ldq > ld_max || ldk > ld_max || ldv > ld_max || ldo > ld_max || (key_mask && ld_mask < Skv))
+    return W4A4_ERR_SHAPE;
+  // strides of the tensor maps and tile counts stay within their fields
+  const int64_t bytes_max = int64_t(1) << 39;
+  if (Sq * ldq >= bytes_max || Skv * ldk >= bytes_max || Skv * ldv >= bytes_max || Sq * ldo >= bytes_max ||
+      batch * heads * ceil_div(Sq, 4) > (int64_t(1) << 30))
+    return W4A4_ERR_SHAPE;
+  if (!(softmax_scale > 0.0f) || !(softmax_scale < 3.0e38f)) return W4A4_ERR_ARG;
+  if (batch == 0 || Sq == 0) return W4A4_OK;
+  if (!O || (Skv > 0 && (!Q || !K || !V))) return W4A4_ERR_NULL;
+  if (!aligned16(Q) || !aligned16(K) || !aligned16(V) || !aligned16(O) || reinterpret_cast<uintptr_t>(kv_len) % 4 != 0)
+    return W4A4_ERR_ALIGN;
+  DeviceInfo* dev = nullptr;
+  int st = device_setup(&dev);
+  if (st != W4A4_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (Skv == 0) {  // no keys: every row is 0
+    if (cudaMemset2DAsync(O, static_cast<size_t>(ldo) * 2, 0, static_cast<size_t>(wq) * 2,
+                          static_cast<size_t>(batch * Sq), s) != cudaSuccess) {
+      cudaGetLastError();
+      return W4A4_ERR_CUDA;
+    }
+    return W4A4_OK;
+  }
+  XAttnParams p = {};
+  p.Sq = static_cast<int>(Sq);
+  p.Skv = static_cast<int>(Skv);
+  p.heads = static_cast<int>(heads);
+  p.kv_heads = static_cast<int>(kv_heads);
+  p.D = static_cast<int>(d_head);
+  const int64_t group = heads / kv_heads;
+  p.pack = 1;
+  while (p.pack < 32 && group % (2 * p.pack) == 0) p.pack *= 2;
+  p.batch = static_cast<int>(batch);
+  p.kv_batch = static_cast<int>(kv_batch);
+  p.kv_len = kv_len;
+  p.key_mask = key_mask;
+  p.ld_mask = ld_mask;
+  p.scale = softmax_scale;
+  p.O = static_cast<__nv_bfloat16*>(O);
+  p.ldo = ldo;
+  p.status = dev->status_ptr;
+  const XPlan plan = xattn_plan(Sq * p.pack, batch * (heads / p.pack), ceil_div(Skv, kXTile), dev->num_sms);
+  if (plan.splits > 0)
+    return d_head <= 64
+               ? launch_cross_attention<XAttnCfg<1, true>>(Q, ldq, K, ldk, V, ldv, p, plan.splits, s, dev)
+               : launch_cross_attention<XAttnCfg<2, true>>(Q, ldq, K, ldk, V, ldv, p, plan.splits, s, dev);
+  return d_head <= 64 ? launch_cross_attention<XAttnCfg<1, false>>(Q, ldq, K, ldk, V, ldv, p, 1, s, dev)
+                      : launch_cross_attention<XAttnCfg<2, false>>(Q, ldq, K, ldk, V, ldv, p, 1, s, dev);
 }
 
 int w4a4_fp4_mma_rate(int iters, int pair, unsigned long long* cycles, void* stream) {

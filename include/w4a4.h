@@ -407,6 +407,93 @@ int attention_fp8(const uint8_t* Q8, const uint8_t* K8, const uint8_t* Vt8, int6
                   void* stream);
 
 /*
+ * The layers around the W4A4 ones: residual addition and norm, layers kept in
+ * 8 bits, cross attention.  The pages name none of their arithmetic; a
+ * transformer block needs them beside its W4A4 projections (layers whose
+ * quantisation error matters most stay in a wider format), and what is
+ * written here fixes it.
+ *
+ * fp8_quantize_rows -- bf16 X [rows, cols] (row stride ldx elements) to E4M3
+ * codes with one fp32 scale per row: s = max|x| / 448 over the row (1 when
+ * that is not a normal number), code = E4M3_rn_satfinite(x * (1 / s)).  For
+ * the weights and the activations of fp8_gemm.  NaN elements do not count for
+ * the maximum and give the NaN code.
+ *   cols % 8 == 0, cols <= W4A4_MAX_ROW_COLS, ldx >= cols, ldx % 8 == 0
+ *   codes   out [rows, ldo bytes], ldo >= cols, ldo % 8 == 0 (fp8_gemm reads
+ *           rows of a multiple of 16 columns and bytes)
+ *   scales  out fp32 [rows]
+ */
+#define W4A4_MAX_ROW_COLS ((int64_t)32768)
+int fp8_quantize_rows(const void* X, int64_t rows, int64_t cols, int64_t ldx, uint8_t* codes, int64_t ldo,
+                      float* scales, void* stream);
+
+/*
+ * rmsnorm_fp8 -- residual addition, root-mean-square norm and row codes in
+ * one pass:  h = x + r;  y = h / sqrt(sum(h^2) / cols + eps) * weight;
+ * codes and scales of y as fp8_quantize_rows gives them, from y in fp32
+ * (nothing is rounded to bf16 on the way).
+ *   X, R      in  bf16 [rows, ldx / ldr] (R NULL: no addition)
+ *   weight    in  bf16 [cols] or NULL (ones);  eps finite and >= 0
+ *   hidden    out bf16(h) [rows, ldh] or NULL; may be X or R itself (same
+ *                 pointer and stride)
+ *   normed    out bf16(y) [rows, ldn] or NULL (the input of
+ *                 nvfp4_quantize_act, for a W4A4 layer after the norm)
+ *   codes, scales  out as in fp8_quantize_rows; codes NULL: neither is
+ *                 written (then normed must be given)
+ * Sizes and strides as in fp8_quantize_rows.
+ */
+int rmsnorm_fp8(const void* X, int64_t rows, int64_t cols, int64_t ldx, const void* R, int64_t ldr,
+                const void* weight, float eps, void* hidden, int64_t ldh, void* normed, int64_t ldn,
+                uint8_t* codes, int64_t ldo, float* scales, void* stream);
+
+/*
+ * fp8_gemm -- a linear layer on E4M3 codes with row scales:
+ *   Y[m,n] = bf16( act( s_a[m] s_w[n] sum_k dec(A8[m,k]) dec(W8[n,k]) + bias[n] ) + R[m,n] )
+ * on the FP8 tensor cores, accumulated in fp32 and rounded once.
+ *   A8   in  E4M3 [M, lda bytes];  s_a fp32 [M] (s_a_rows = 1), or one device
+ *            scalar for all of A (s_a_rows = 0, e.g. from fp8_quantize)
+ *   W8   in  E4M3 [N, ldw bytes];  s_w fp32 [N], 16-byte aligned
+ *   bias in  bf16 [N] or NULL;  epilogue: W4A4_EPI_NONE or W4A4_EPI_GELU_TANH
+ *   R    in  bf16 [M, ldr] residual or NULL; may be Y itself (same pointer
+ *            and stride)
+ *   Y    out bf16 [M, ldy]
+ *   K % 16 == 0, K <= W4A4_MAX_K, N % 8 == 0, lda / ldw % 16 == 0, ldr / ldy % 8 == 0
+ * Up to 128 rows: the weight streams past the tokens, K split over a cluster
+ * of CTAs whose partial sums are added in slice order (deterministic); more:
+ * CTA pairs with 256-row tiles.
+ */
+int fp8_gemm(const uint8_t* A8, int64_t lda, const float* s_a, int s_a_rows, int64_t M, int64_t N, int64_t K,
+             const uint8_t* W8, int64_t ldw, const float* s_w, const void* bias, int epilogue, const void* R,
+             int64_t ldr, void* Y, int64_t ldy, void* stream);
+
+/*
+ * cross_attention_bf16 -- O = softmax(c Q K^T) V per head and sequence, the
+ * queries' length and the keys' length each their own (image tokens against
+ * an encoder's states):
+ *   Q     in  bf16 [batch * Sq, ldq], token-major, head h in columns h*d_head ..
+ *   K, V  in  bf16 [kv_batch * Skv, ldk / ldv]; key/value head h / (heads /
+ *             kv_heads) serves query head h (heads % kv_heads == 0); kv_batch
+ *             is batch, or 1: every sequence attends to the same states
+ *   d_head    a multiple of 8, 8 .. 128
+ *   kv_len    in  int32 device [kv_batch] or NULL: only the first kv_len[b]
+ *             keys count (values outside 0 .. Skv are taken as the nearest)
+ *   key_mask  in  uint8 device [kv_batch, ld_mask] or NULL: keys with 0 do
+ *             not count
+ *   softmax_scale  c (normally 1/sqrt(d_head)), finite and > 0
+ *   O     out bf16 [batch * Sq, ldo]
+ * Keys that do not count may hold anything, NaN included.  A query without a
+ * key gets 0.  A counted score that is NaN or +infinity makes its row NaN.
+ * fp32 scores, sums and accumulation; the probabilities are rounded to bf16
+ * for the second product.  Strides are in elements, multiples of 8 (ld_mask:
+ * any, >= Skv); Sq, Skv <= 2^24.  No workspace; results do not depend on
+ * timing.
+ */
+int cross_attention_bf16(const void* Q, int64_t ldq, const void* K, int64_t ldk, const void* V, int64_t ldv,
+                         int64_t batch, int64_t kv_batch, int64_t Sq, int64_t Skv, int64_t heads, int64_t kv_heads,
+                         int64_t d_head, const int* kv_len, const uint8_t* key_mask, int64_t ld_mask,
+                         float softmax_scale, void* O, int64_t ldo, void* stream);
+
+/*
  * w4a4_fp4_mma_rate -- a measurement, not part of the layer: the rate of the
  * block-scaled FP4 tensor-core instruction the GEMM is built on
  * (tcgen05.mma kind::mxf4nvf4.block_scale.block16), issued back to back with
