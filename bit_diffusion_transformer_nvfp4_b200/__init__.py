@@ -457,44 +457,43 @@ def attention(q: Fp8Tensor, k: Fp8Tensor, vt: Fp8Tensor, heads: int, batch: int 
     return O
 
 
-def _matrix(name, t, dtype, rows=None, cols=None, device=None):
-    """The row stride of a 2-D tensor of the given type whose rows are
-    contiguous; raises on anything the kernels would misread."""
-    if t.dtype != dtype:
+def _matrix(name, t, dtype, dev, rows=None, cols=None):
+    """The row stride of a 2-D tensor of the given type on CUDA device ``dev``
+    whose rows are contiguous; raises on anything the kernels would misread."""
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: {dtype} expected, got {t.dtype}")
-    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
+    shape = t.shape
+    if len(shape) != 2 or (rows is not None and shape[0] != rows) or (cols is not None and shape[1] != cols):
         raise ValueError(f"{name}: shape [{'*' if rows is None else rows}, {'*' if cols is None else cols}] expected, "
-                         f"got {list(t.shape)}")
-    if t.device.type != "cuda" or (device is not None and t.device != device):
-        raise ValueError(f"{name}: on {t.device}, expected {device or 'a CUDA device'}")
-    r, c = t.shape
-    if c > 1 and t.stride(1) != 1 or r > 1 and t.stride(0) < c:
+                         f"got {list(shape)}")
+    if dev < 0 or t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, expected {f'cuda:{dev}' if dev >= 0 else 'a CUDA device'}")
+    r, c = shape
+    ld, inner = t.stride()
+    if inner != 1 and c > 1 or ld < c and r > 1:
         raise ValueError(f"{name}: contiguous rows expected, got strides {t.stride()}")
-    return t.stride(0) if r > 1 else -(-c // 16) * 16  # (one row: its stride never matters)
+    return ld if r > 1 else -(-c // 16) * 16  # (one row: its stride never matters)
 
 
-def _vector(name, t, dtype, n, device):
-    if t.dtype != dtype or t.shape != (n,) or t.device != device or (n > 1 and t.stride(0) != 1):
-        raise ValueError(f"{name}: contiguous {dtype} [{n}] on {device} expected, got {t.dtype} {list(t.shape)} with "
+def _vector(name, t, dtype, dev, n):
+    if t.dtype is not dtype or t.shape != (n,) or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous {dtype} [{n}] on cuda:{dev} expected, got {t.dtype} {list(t.shape)} with "
                          f"strides {t.stride()} on {t.device}")
 
 
-class _on:
-    """Makes a tensor's device current for a call (the library works on the
-    current device)."""
-
-    def __init__(self, device):
-        self.index = device.index
-        self.back = None
-
-    def __enter__(self):
-        if torch.cuda.current_device() != self.index:
-            self.back = torch.cuda.current_device()
-            torch.cuda.set_device(self.index)
-
-    def __exit__(self, *exc):
-        if self.back is not None:
-            torch.cuda.set_device(self.back)
+def _launch(fn, dev, stream, *args):
+    """Calls an entry point with ``dev`` current (the library works on the
+    current device) on the given stream or ``dev``'s current one."""
+    current = torch.cuda.current_device()
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        stream = getattr(stream, "cuda_stream", stream)
+    if current == dev:
+        _check(fn, getattr(lib(), fn)(*args, stream))
+        return
+    with torch.cuda.device(dev):
+        _check(fn, getattr(lib(), fn)(*args, stream))
 
 
 class Fp8Rows:
@@ -514,20 +513,27 @@ class PackedWeightFp8:
         self.N, self.K = codes.shape
 
 
+def _row_outputs(rows, cols, dev, device, codes, scales):
+    """(codes, their row stride, scales), made where they are None."""
+    if codes is None:
+        codes, ldo = torch.empty((rows, cols), dtype=torch.uint8, device=device), cols
+    else:
+        ldo = _matrix("codes", codes, torch.uint8, dev, rows, cols)
+    if scales is None:
+        scales = torch.empty(rows, dtype=torch.float32, device=device)
+    else:
+        _vector("scales", scales, torch.float32, dev, rows)
+    return codes, ldo, scales
+
+
 def quantize_rows_fp8(X, codes=None, scales=None, stream=None) -> Fp8Rows:
     """E4M3 codes of a bf16 [rows, cols] view, one scale per row (cols a
     multiple of 8, at most MAX_ROW_COLS)."""
-    ldx = _matrix("X", X, torch.bfloat16)
+    dev = X.get_device()
+    ldx = _matrix("X", X, torch.bfloat16, dev)
     rows, cols = X.shape
-    dev = X.device
-    if codes is None:
-        codes = torch.empty(rows, cols, dtype=torch.uint8, device=dev)
-    if scales is None:
-        scales = torch.empty(rows, dtype=torch.float32, device=dev)
-    ldo = _matrix("codes", codes, torch.uint8, rows, cols, dev)
-    _vector("scales", scales, torch.float32, rows, dev)
-    with _on(dev):
-        fp8_quantize_rows(X, rows, cols, ldx, codes, ldo, scales, stream)
+    codes, ldo, scales = _row_outputs(rows, cols, dev, X.device, codes, scales)
+    _launch("fp8_quantize_rows", dev, stream, X.data_ptr(), rows, cols, ldx, codes.data_ptr(), ldo, scales.data_ptr())
     return Fp8Rows(codes, scales)
 
 
@@ -539,29 +545,29 @@ def rms_norm_fp8(X, weight=None, residual=None, eps=1e-6, hidden=None, normed=No
     (in place with ``hidden=X`` or ``hidden=residual``), else None unless a
     tensor is passed.  ``normed``: a bf16 tensor that also receives the norm
     itself, for a W4A4 layer behind it (``quantize_act``)."""
-    ldx = _matrix("X", X, torch.bfloat16)
+    dev = X.get_device()
+    ldx = _matrix("X", X, torch.bfloat16, dev)
     rows, cols = X.shape
-    dev = X.device
     ldr = ldh = ldn = 0
+    r = h = n = w = None
     if residual is not None:
-        ldr = _matrix("residual", residual, torch.bfloat16, rows, cols, dev)
-        if hidden is None:
-            hidden = torch.empty(rows, cols, dtype=torch.bfloat16, device=dev)
+        ldr = _matrix("residual", residual, torch.bfloat16, dev, rows, cols)
+        r = residual.data_ptr()
     if hidden is not None:
-        ldh = _matrix("hidden", hidden, torch.bfloat16, rows, cols, dev)
+        ldh = _matrix("hidden", hidden, torch.bfloat16, dev, rows, cols)
+    elif residual is not None:
+        hidden, ldh = torch.empty((rows, cols), dtype=torch.bfloat16, device=X.device), cols
+    if hidden is not None:
+        h = hidden.data_ptr()
     if normed is not None:
-        ldn = _matrix("normed", normed, torch.bfloat16, rows, cols, dev)
+        ldn = _matrix("normed", normed, torch.bfloat16, dev, rows, cols)
+        n = normed.data_ptr()
     if weight is not None:
-        _vector("weight", weight, torch.bfloat16, cols, dev)
-    if codes is None:
-        codes = torch.empty(rows, cols, dtype=torch.uint8, device=dev)
-    if scales is None:
-        scales = torch.empty(rows, dtype=torch.float32, device=dev)
-    ldo = _matrix("codes", codes, torch.uint8, rows, cols, dev)
-    _vector("scales", scales, torch.float32, rows, dev)
-    with _on(dev):
-        rmsnorm_fp8(X, rows, cols, ldx, residual, ldr, weight, eps, hidden, ldh, normed, ldn, codes, ldo, scales,
-                    stream)
+        _vector("weight", weight, torch.bfloat16, dev, cols)
+        w = weight.data_ptr()
+    codes, ldo, scales = _row_outputs(rows, cols, dev, X.device, codes, scales)
+    _launch("rmsnorm_fp8", dev, stream, X.data_ptr(), rows, cols, ldx, r, ldr, w, eps, h, ldh, n, ldn,
+            codes.data_ptr(), ldo, scales.data_ptr())
     return Fp8Rows(codes, scales), hidden
 
 
@@ -578,24 +584,27 @@ def linear_fp8(a, w: PackedWeightFp8, activation: int = EPI_NONE, residual=None,
     per_row = isinstance(a, Fp8Rows)
     if not per_row and a.transposed:
         raise ValueError("a: row-major codes expected")
-    codes = a.codes
-    lda = _matrix("a.codes", codes, torch.uint8, None, w.K)
-    M, dev = codes.shape[0], codes.device
-    ldw = _matrix("w.codes", w.codes, torch.uint8, w.N, w.K, dev)
+    codes, N, K = a.codes, w.N, w.K
+    dev = codes.get_device()
+    lda = _matrix("a.codes", codes, torch.uint8, dev, None, K)
+    M = codes.shape[0]
+    ldw = _matrix("w.codes", w.codes, torch.uint8, dev, N, K)
     s_a = a.scales if per_row else a.scale
-    _vector("a.scales", s_a, torch.float32, M if per_row else 1, dev)
-    _vector("w.scales", w.scales, torch.float32, w.N, dev)
+    _vector("a.scales", s_a, torch.float32, dev, M if per_row else 1)
+    _vector("w.scales", w.scales, torch.float32, dev, N)
+    ldr, b, r = 0, None, None
     if w.bias is not None:
-        _vector("w.bias", w.bias, torch.bfloat16, w.N, dev)
-    ldr = 0
+        _vector("w.bias", w.bias, torch.bfloat16, dev, N)
+        b = w.bias.data_ptr()
     if residual is not None:
-        ldr = _matrix("residual", residual, torch.bfloat16, M, w.N, dev)
+        ldr = _matrix("residual", residual, torch.bfloat16, dev, M, N)
+        r = residual.data_ptr()
     if Y is None:
-        Y = torch.empty(M, w.N, dtype=torch.bfloat16, device=dev)
-    ldy = _matrix("Y", Y, torch.bfloat16, M, w.N, dev)
-    with _on(dev):
-        fp8_gemm(codes, lda, s_a, int(per_row), M, w.N, w.K, w.codes, ldw, w.scales, w.bias, activation, residual,
-                 ldr, Y, ldy, stream)
+        Y, ldy = torch.empty((M, N), dtype=torch.bfloat16, device=codes.device), N
+    else:
+        ldy = _matrix("Y", Y, torch.bfloat16, dev, M, N)
+    _launch("fp8_gemm", dev, stream, codes.data_ptr(), lda, s_a.data_ptr(), int(per_row), M, N, K, w.codes.data_ptr(),
+            ldw, w.scales.data_ptr(), b, activation, r, ldr, Y.data_ptr(), ldy)
     return Y
 
 
@@ -610,29 +619,34 @@ def cross_attention(q, k, v, heads: int, kv_heads=None, batch: int = 1, kv_batch
     [batch*Sq, heads*d]; a query without keys gets 0."""
     kv_heads = heads if kv_heads is None else kv_heads
     kv_batch = batch if kv_batch is None else kv_batch
-    ldq = _matrix("q", q, torch.bfloat16)
-    dev = q.device
-    if heads < 1 or kv_heads < 1 or batch < 1 or kv_batch < 1 or q.shape[1] % heads or q.shape[0] % batch:
+    dev = q.get_device()
+    ldq = _matrix("q", q, torch.bfloat16, dev)
+    rows, width = q.shape
+    if heads < 1 or kv_heads < 1 or batch < 1 or kv_batch < 1 or width % heads or rows % batch:
         raise ValueError(f"q {list(q.shape)} does not divide into {batch} sequences of {heads} heads")
-    d, Sq = q.shape[1] // heads, q.shape[0] // batch
-    ldk = _matrix("k", k, torch.bfloat16, None, kv_heads * d, dev)
-    if k.shape[0] % kv_batch:
+    d = width // heads
+    ldk = _matrix("k", k, torch.bfloat16, dev, None, kv_heads * d)
+    keys = k.shape[0]
+    if keys % kv_batch:
         raise ValueError(f"k {list(k.shape)} does not divide into {kv_batch} sequences")
-    Skv = k.shape[0] // kv_batch
-    ldv = _matrix("v", v, torch.bfloat16, k.shape[0], kv_heads * d, dev)
-    if kv_len is not None:
-        _vector("kv_len", kv_len, torch.int32, kv_batch, dev)
+    Skv = keys // kv_batch
+    ldv = _matrix("v", v, torch.bfloat16, dev, keys, kv_heads * d)
+    n = m = None
     ldm = 0
+    if kv_len is not None:
+        _vector("kv_len", kv_len, torch.int32, dev, kv_batch)
+        n = kv_len.data_ptr()
     if key_mask is not None:
-        ldm = max(Skv, _matrix("key_mask", key_mask, torch.uint8 if key_mask.dtype == torch.uint8 else torch.bool,
-                               kv_batch, Skv, dev))
+        ldm = max(Skv, _matrix("key_mask", key_mask, torch.uint8 if key_mask.dtype is torch.uint8 else torch.bool, dev,
+                               kv_batch, Skv))
+        m = key_mask.data_ptr()
     if O is None:
-        O = torch.empty(q.shape[0], heads * d, dtype=torch.bfloat16, device=dev)
-    ldo = _matrix("O", O, torch.bfloat16, q.shape[0], heads * d, dev)
+        O, ldo = torch.empty((rows, width), dtype=torch.bfloat16, device=q.device), width
+    else:
+        ldo = _matrix("O", O, torch.bfloat16, dev, rows, width)
     c = 1.0 / math.sqrt(d) if softmax_scale is None else softmax_scale
-    with _on(dev):
-        cross_attention_bf16(q, ldq, k, ldk, v, ldv, batch, kv_batch, Sq, Skv, heads, kv_heads, d, kv_len, key_mask,
-                             ldm, c, O, ldo, stream)
+    _launch("cross_attention_bf16", dev, stream, q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, batch,
+            kv_batch, rows // batch, Skv, heads, kv_heads, d, n, m, ldm, c, O.data_ptr(), ldo)
     return O
 
 

@@ -17,7 +17,9 @@
 // TMEM; P goes back into S's columns as the A operand of the second product,
 // V is its MN-major B operand as it lies in memory.  MMAs of the issuing
 // thread run in order, so S of the next key tile may follow the product that
-// reads P, and a commit that covers S covers the product before it too.
+// reads P, and a commit that covers S covers the product before it too; each
+// stream has an issuing warp of its own (issuing takes 45 to 58 cycles an
+// MMA and a wait about 100, so one warp for both left the tensor pipe idle).
 //
 // Two forms, each with two streams of softmax (a warpgroup each, one row a
 // thread) that alternate on the tensor cores:
@@ -34,11 +36,15 @@
 
 namespace w4a4 {
 
-constexpr int kXTile = 128;       // rows per stream, keys per step
-constexpr int kXThreads = 384;    // control warpgroup, two softmax warpgroups
+constexpr int kXTile = 128;       // rows per stream, keys of a ring slot
+constexpr int kXSub = 64;         // keys of a score buffer
+constexpr int kXThreads = 512;    // control warpgroup, a softmax warpgroup a stream, epilogue warpgroup
 constexpr float kXSlack = 8.0f;   // binades a tile's maximum may pass the offset
-constexpr int kXRegsCtrl = 48, kXRegsSoftmax = 224;
-static_assert(128 * kXRegsCtrl + 256 * kXRegsSoftmax <= kXThreads * 168, "register budgets fit the launch allocation");
+constexpr int kXChunk = 16;       // scores taken together through the exponential
+constexpr int kXPolyPairs = 2;    // of 16 pairs of exponentials, how many on the FMA pipes instead of the MUFU
+constexpr int kXRegsCtrl = 64, kXRegsSoftmax = 168, kXRegsEpi = 112;  // of 128 at launch
+static_assert(128 * (kXRegsCtrl + kXRegsEpi) + 256 * kXRegsSoftmax <= kXThreads * 128,
+              "register budgets fit the launch allocation");
 
 struct XAttnParams {
   int Sq, Skv, heads, kv_heads, D;
@@ -65,12 +71,13 @@ struct XAttnCfg {
   static constexpr int Q_OFF = 0;
   static constexpr int KV_OFF = NQ * TILE_BYTES;
   static constexpr int O_OFF = KV_OFF + SLOTS * TILE_BYTES;
-  static constexpr int O_BYTES = SPLIT ? 0 : 8 * 32 * 128;       // a 32 x 64 bf16 box per softmax warp
+  static constexpr int O_BYTES = SPLIT ? 0 : 8 * 32 * 128;       // two 32 x 64 bf16 boxes per epilogue warp
   static constexpr int PART_PITCH = DB * 64 + 4;                 // floats; SPLIT: over Q and the ring
   static constexpr int STAT_OFF = 2 * kXTile * PART_PITCH * 4;   // behind them m and l, [2 streams][2][128]
-  static constexpr int BAR_OFF = O_OFF + O_BYTES;
-  static constexpr int BARS = 2 * SLOTS + 2 * 5 + 1;
-  static constexpr int SMEM = BAR_OFF + 8 * BARS + 16 + 1024;
+  static constexpr int F_OFF = O_OFF + O_BYTES;                  // the rows' final factors, [2 streams][128]
+  static constexpr int BAR_OFF = F_OFF + (SPLIT ? 0 : 2 * kXTile * 4);
+  static constexpr int BARS = 2 * SLOTS + 2 * 10;
+  static constexpr int SMEM = BAR_OFF + 8 * BARS + 8;  // (no slack: the kernel checks its base)
   static constexpr int TMEM_COLS = 512;
   static constexpr int O_COL = 256;        // S of stream t at 128 t, O at 256 + 128 t
   static_assert(SMEM <= 232448, "shared memory budget");
@@ -139,6 +146,13 @@ __device__ __forceinline__ XTileAt xattn_tile(const XAttnParams& p, int tile, in
   return a;
 }
 
+// Key tiles [j0, j1) of `len` keys that fall to one of `splits` CTAs.
+__device__ __forceinline__ void xattn_key_range(int len, int split, int splits, int& j0, int& j1) {
+  const int n = (len + kXTile - 1) / kXTile;
+  j0 = static_cast<int>(static_cast<int64_t>(n) * split / splits);
+  j1 = static_cast<int>(static_cast<int64_t>(n) * (split + 1) / splits);
+}
+
 template <class C>
 __global__ void __launch_bounds__(kXThreads, 1)
     cross_attention_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -149,32 +163,45 @@ __global__ void __launch_bounds__(kXThreads, 1)
   constexpr int kRows = SPLIT ? kXTile : 2 * kXTile;  // rows of a work tile
   grid_launch_dependents();
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* smem = smem_raw;
+  if ((smem_u32(smem_raw) & 1023u) != 0) {
+    // the swizzled tiles need 1024-byte alignment; every CTA sees the same
+    // base, so all return here before any barrier or TMEM use
+    grid_dependency_wait();
+    if (threadIdx.x == 0 && p.status) atomicExch(p.status, kStatusMisaligned);
+    return;
+  }
   uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);  // [SLOTS]
   uint64_t* kv_empty = kv_full + SLOTS;                                 // [SLOTS]
   uint64_t* q_full = kv_empty + SLOTS;                                  // [2] query tiles (SPLIT: the first)
   uint64_t* q_empty = q_full + 2;                                       // [2] the tile's last scores are done
-  uint64_t* s_full = q_empty + 2;                                       // [2] per stream: scores in TMEM
-  uint64_t* p_full = s_full + 2;                                        // [2] probabilities in TMEM, O rescaled
-  uint64_t* o_done = p_full + 2;                                        // [2] the tile's last product is done
-  uint64_t* drain = o_done + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* s_full = q_empty + 2;                                       // [2][2] per stream and buffer: scores
+  uint64_t* p_full = s_full + 4;                                        // [2][2] probabilities, O rescaled
+  uint64_t* o_done = p_full + 4;                                        // [2] the tile's last product is done
+  uint64_t* f_full = o_done + 2;                                        // [2] its rows' factors are there
+  uint64_t* o_free = f_full + 2;                                        // [2] its sums and factors have been read
+  uint64_t* drain = o_free + 2;                                         // [2] the issuers' last commits
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // (warp: uniform)
   if (threadIdx.x == 0) {
     for (int s = 0; s < SLOTS; ++s) {
       mbar_init(smem_u32(&kv_full[s]), 1);
-      mbar_init(smem_u32(&kv_empty[s]), 1);
+      mbar_init(smem_u32(&kv_empty[s]), SPLIT ? 1 : 2);  // the streams that read the slot
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(smem_u32(&q_full[t]), 1);
       mbar_init(smem_u32(&q_empty[t]), 1);
-      mbar_init(smem_u32(&s_full[t]), 1);
-      mbar_init(smem_u32(&p_full[t]), 4);
+      for (int w = 0; w < 2; ++w) {
+        mbar_init(smem_u32(&s_full[2 * t + w]), 1);
+        mbar_init(smem_u32(&p_full[2 * t + w]), 4);
+      }
       mbar_init(smem_u32(&o_done[t]), 1);
+      mbar_init(smem_u32(&f_full[t]), 4);
+      mbar_init(smem_u32(&o_free[t]), 4);
     }
-    mbar_init(smem_u32(drain), 1);
+    for (int t = 0; t < 2; ++t) mbar_init(smem_u32(&drain[t]), 1);
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tm_q);
@@ -198,20 +225,14 @@ __global__ void __launch_bounds__(kXThreads, 1)
   const int split = SPLIT ? static_cast<int>(blockIdx.x) : 0;
   const int first = SPLIT ? static_cast<int>(blockIdx.y) : static_cast<int>(blockIdx.x);
   const int step = SPLIT ? p.tiles : static_cast<int>(gridDim.x);
-  // key tiles [j0, j1) of a tile with `len` keys
-  auto key_range = [&](int len, int& j0, int& j1) {
-    const int n = (len + kXTile - 1) / kXTile;
-    j0 = SPLIT ? static_cast<int>(static_cast<int64_t>(n) * split / splits) : 0;
-    j1 = SPLIT ? static_cast<int>(static_cast<int64_t>(n) * (split + 1) / splits) : n;
-  };
 
   if (warp < 4) {
     regs_release_to<kXRegsCtrl>();
     if (warp == 0 && lane == 0) {
-      // ---------------------------------------------------------- TMA producer
-      uint32_t fill = 0, nonempty = 0;
+      // ---------------------------------------------------------- keys and values
+      uint32_t fill = 0;
       bool ok = true;
-      auto load_kv = [&](const CUtensorMap* map, const XTileAt& a, int j) {
+      auto load = [&](const CUtensorMap* map, const XTileAt& a, int j) {
         const uint32_t s = fill % SLOTS;
         if (!ok || !(ok = mbar_wait(smem_u32(&kv_empty[s]), ((fill / SLOTS) & 1) ^ 1, abort_flag, p.status))) return;
         const uint32_t bar = smem_u32(&kv_full[s]);
@@ -222,173 +243,193 @@ __global__ void __launch_bounds__(kXThreads, 1)
                       j * kXTile, a.kb);
         ++fill;
       };
-      uint32_t q_fills = 0;
-      auto load_q = [&](const XTileAt& a, int t) {
-        if (!ok || !(ok = mbar_wait(smem_u32(&q_empty[t]), (nonempty & 1) ^ 1, abort_flag, p.status))) return;
-        const uint32_t bar = smem_u32(&q_full[t]);
-        mbar_arrive_expect_tx(bar, C::TILE_BYTES);
-#pragma unroll
-        for (int d = 0; d < DB; ++d)
-          tma_load_4d(smem_u32(smem + C::Q_OFF + t * C::TILE_BYTES + d * (kXTile * 128)), &tm_q, bar, 64 * d, a.h0,
-                      (a.row0 + t * kXTile) / p.pack, a.b);
-        q_fills |= 1u << t;
-      };
       for (int tile = first; tile < p.tiles && ok; tile += step) {
         const XTileAt a = xattn_tile(p, tile, kRows);
         int j0, j1;
-        key_range(a.len, j0, j1);
-        if (j0 == j1) continue;
-        q_fills = 0;
-        load_q(a, 0);
+        xattn_key_range(a.len, split, splits, j0, j1);
         if (SPLIT) {
           // consumed in the order K0 K1 V0 K2 V1 K3 ...
-          for (int j = j0; j <= j1 && ok; ++j) {
-            if (j < j1) load_kv(&tm_k, a, j);
-            if (j > j0) load_kv(&tm_v, a, j - 1);
+          for (int j = j0; j0 < j1 && j <= j1 && ok; ++j) {
+            if (j < j1) load(&tm_k, a, j);
+            if (j > j0) load(&tm_v, a, j - 1);
           }
         } else {
           for (int j = j0; j < j1 && ok; ++j) {
-            load_kv(&tm_k, a, j);
-            if (j == j0) load_q(a, 1);
-            load_kv(&tm_v, a, j);
+            load(&tm_k, a, j);
+            load(&tm_v, a, j);
           }
         }
-        if (ok) ++nonempty;
       }
       // every fill issued lands before the shared memory is released
       for (uint32_t j = fill > SLOTS ? fill - SLOTS : 0u; j < fill; ++j)
         mbar_wait_drain(smem_u32(&kv_full[j % SLOTS]), (j / SLOTS) & 1);
-      if (!ok)
-        for (int t = 0; t < 2; ++t)
-          if (q_fills >> t & 1) mbar_wait_drain(smem_u32(&q_full[t]), nonempty & 1);
-    } else if (warp == 1 && lane == 0) {
-      // ---------------------------------------------------------- MMA issuer
-      constexpr uint32_t kIdescS = idesc_bf16(kXTile, kXTile);
-      constexpr uint32_t kIdescO = idesc_bf16(kXTile, DB * 64) | (1u << 16);  // B (the values) MN-major
-      const int d_steps = (p.D + 15) / 16;
-      uint32_t use = 0;  // ring slots consumed
+    } else if (warp == 3 && lane == 0) {
+      // ---------------------------------------------------------- queries
+      // (a thread of their own: a query tile waits for the scores of the
+      // work tile before, and would hold up the keys and values behind it)
+      uint32_t fills[2] = {0u, 0u};
       bool ok = true;
-      auto slot_wait = [&](uint32_t n) -> bool {
-        return mbar_wait(smem_u32(&kv_full[n % SLOTS]), (n / SLOTS) & 1, abort_flag, p.status);
-      };
-      auto slot_base = [&](uint32_t n) -> uint32_t {
-        return smem_u32(smem + C::KV_OFF + (n % SLOTS) * C::TILE_BYTES);
-      };
-      auto scores = [&](int t, uint32_t n) {  // S_t = Q K^T, keys in ring slot n
-        tc_fence_after();
-        const uint32_t q = smem_u32(smem + C::Q_OFF + (SPLIT ? 0 : t) * C::TILE_BYTES), k = slot_base(n);
+      for (int tile = first; tile < p.tiles && ok; tile += step) {
+        const XTileAt a = xattn_tile(p, tile, kRows);
+        int j0, j1;
+        xattn_key_range(a.len, split, splits, j0, j1);
+        if (j0 == j1) continue;
 #pragma unroll
-        for (int i = 0; i < DB * 4; ++i)
-          if (i < d_steps)
-            mma_bf16(tmem + 128 * t, smem_desc(q + (i / 4) * (kXTile * 128) + 32 * (i % 4), 16, 1024, kSwizzle128B),
-                     smem_desc(k + (i / 4) * (kXTile * 128) + 32 * (i % 4), 16, 1024, kSwizzle128B), kIdescS,
-                     i > 0 ? 1u : 0u);
-        tc_commit(smem_u32(&s_full[t]));
-      };
-      auto product = [&](int t, uint32_t n, bool fresh) {  // O_t (+)= P_t V, values in ring slot n
-        tc_fence_after();
-        const uint32_t v = slot_base(n);
+        for (int t = 0; t < (SPLIT ? 1 : 2); ++t) {
+          if (!ok || !(ok = mbar_wait(smem_u32(&q_empty[t]), (fills[t] & 1) ^ 1, abort_flag, p.status))) break;
+          const uint32_t bar = smem_u32(&q_full[t]);
+          mbar_arrive_expect_tx(bar, C::TILE_BYTES);
 #pragma unroll
-        for (int i = 0; i < kXTile / 16; ++i)
-          mma_bf16_ts(tmem + C::O_COL + 128 * t, tmem + 128 * t + 8 * i,
-                      smem_desc(v + 2048 * i, kXTile * 128, 1024, kSwizzle128B), kIdescO,
-                      (!fresh || i > 0) ? 1u : 0u);
+          for (int d = 0; d < DB; ++d)
+            tma_load_4d(smem_u32(smem + C::Q_OFF + t * C::TILE_BYTES + d * (kXTile * 128)), &tm_q, bar, 64 * d, a.h0,
+                        (a.row0 + t * kXTile) / p.pack, a.b);
+          ++fills[t];
+        }
+        if (!SPLIT && tile + step < p.tiles) {
+          // the next tile's towards L2 meanwhile
+          const XTileAt z = xattn_tile(p, tile + step, kRows);
+          for (int t = 0; t < 2; ++t)
+            if ((z.row0 + t * kXTile) / p.pack < p.Sq)
+              for (int d = 0; d < DB; ++d)
+                tma_prefetch_4d(&tm_q, 64 * d, z.h0, (z.row0 + t * kXTile) / p.pack, z.b);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        if (fills[t] > 0) mbar_wait_drain(smem_u32(&q_full[t]), (fills[t] - 1) & 1);
+    } else if (warp == 1 || warp == 2) {
+      // ---------------------------------------------------------- MMA issuers, one a stream
+      // (the whole warp in uniform control flow, one elected lane issuing)
+      const int t = warp - 1;
+      constexpr uint32_t kIdescS = idesc_bf16(kXTile, kXSub);
+      constexpr uint32_t kIdescO = idesc_bf16(kXTile, DB * 64) | (1u << 16);  // B (the values) MN-major
+      const uint32_t t_s = tmem + 128 * t, t_o = tmem + C::O_COL + 128 * t;
+      const uint64_t q_desc =
+          smem_desc(smem_u32(smem + C::Q_OFF + (SPLIT ? 0 : t) * C::TILE_BYTES), 16, 1024, kSwizzle128B);
+      const uint64_t k_desc = smem_desc(smem_u32(smem + C::KV_OFF), 16, 1024, kSwizzle128B);
+      const uint64_t v_desc = smem_desc(smem_u32(smem + C::KV_OFF), kXTile * 128, 1024, kSwizzle128B);
+      auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        return mbar_wait_warp(smem_u32(bar), parity & 1, abort_flag, p.status);
       };
-      uint32_t p_phase = 0;  // bit t: parity of the next phase of p_full[t]
-      auto p_wait = [&](int t) -> bool {
-        const bool r = mbar_wait(smem_u32(&p_full[t]), (p_phase >> t) & 1, abort_flag, p.status);
-        p_phase ^= 1u << t;
-        return r;
+      auto slot_wait = [&](uint32_t n) -> bool { return wait(&kv_full[n % SLOTS], n / SLOTS); };
+      // The two halves of a key tile have a score buffer each.  As soon as
+      // the probabilities of a half are there, its product goes out and behind
+      // it the next key tile's scores for the same buffer: two half tiles of
+      // scores are always ahead of the softmax.
+      struct Next {
+        bool live;       // there is a next key tile
+        uint32_t slot;   // its keys
+        bool new_q;      // it opens a work tile
+        bool last;       // it closes one
+      };
+      uint32_t opened = 0;  // work tiles opened
+      auto ready = [&](const Next& k) -> bool {
+        return (!k.new_q || wait(&q_full[SPLIT ? 0 : t], opened)) && slot_wait(k.slot);
+      };
+      auto scores = [&](uint64_t kd, int h) {
+#pragma unroll
+        for (int i = 0; i < DB * 4; ++i)  // (columns past the head's are zeros in both)
+          mma_bf16(t_s + kXSub * h, q_desc + (((i / 4) * (kXTile * 128) + 32 * (i % 4)) >> 4),
+                   kd + (((i / 4) * (kXTile * 128) + 32 * (i % 4) + h * kXSub * 128) >> 4), kIdescS, i > 0 ? 1u : 0u);
+      };
+      auto open = [&](const Next& k) -> bool {  // the first scores of all
+        if (!ready(k)) return false;
+        const uint64_t kd = k_desc + (k.slot % SLOTS) * (C::TILE_BYTES >> 4);
+        tc_fence_after();
+        if (elect_one()) {
+          scores(kd, 0);
+          tc_commit(smem_u32(&s_full[2 * t]));
+          scores(kd, 1);
+          tc_commit(smem_u32(&s_full[2 * t + 1]));
+          tc_commit(smem_u32(&kv_empty[k.slot % SLOTS]));
+          if (k.last) tc_commit(smem_u32(&q_empty[t]));
+        }
+        __syncwarp();
+        ++opened;
+        return true;
+      };
+      uint32_t it = 0, summed = 0;  // key tiles done, work tiles begun
+      auto advance = [&](uint32_t v_slot, bool fresh, const Next& k) -> bool {
+        if (!slot_wait(v_slot)) return false;
+        // the first product of a tile overwrites the sums of the one before
+        if (!SPLIT && fresh && summed++ > 0 && !wait(&o_free[t], summed)) return false;
+        const uint64_t vd = v_desc + (v_slot % SLOTS) * (C::TILE_BYTES >> 4);
+        const uint64_t kd = k_desc + (k.slot % SLOTS) * (C::TILE_BYTES >> 4);
+        const uint32_t v_bar = smem_u32(&kv_empty[v_slot % SLOTS]), k_bar = smem_u32(&kv_empty[k.slot % SLOTS]);
+        const uint32_t add = fresh ? 0u : 1u;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (!wait(&p_full[2 * t + h], it)) return false;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int i = 0; i < kXSub / 16; ++i)
+              mma_bf16_ts(t_o, t_s + kXSub * h + 8 * i, vd + ((2048 * i + h * kXSub * 128) >> 4), kIdescO,
+                          (h > 0 || i > 0) ? 1u : add);
+            if (h == 1) tc_commit(v_bar);
+          }
+          __syncwarp();
+          if (h == 0 && k.live && !ready(k)) return false;
+          tc_fence_after();
+          if (elect_one()) {
+            if (k.live) scores(kd, h);
+            // (without scores behind it too: the product is done)
+            tc_commit(smem_u32(&s_full[2 * t + h]));
+            if (h == 1) {
+              if (k.live) tc_commit(k_bar);
+              if (k.live && k.last) tc_commit(smem_u32(&q_empty[t]));
+              if (!k.live || k.new_q) tc_commit(smem_u32(&o_done[t]));
+            }
+          }
+          __syncwarp();
+        }
+        ++it;
+        if (k.live && k.new_q) ++opened;
+        return true;
       };
       if (SPLIT) {
         if (first < p.tiles) {
           const XTileAt a = xattn_tile(p, first, kRows);
           int j0, j1;
-          key_range(a.len, j0, j1);
-          const int n = j1 - j0;
-          ok = n == 0 || mbar_wait(smem_u32(&q_full[0]), 0, abort_flag, p.status);
-          for (int t = 0; t < 2 && t < n && ok; ++t, ++use) {
-            if (!(ok = slot_wait(use))) break;
-            scores(t, use);
-            tc_commit(smem_u32(&kv_empty[use % SLOTS]));
-          }
-          for (int i = 0; i < n && ok; ++i) {
-            const int t = i & 1;
-            if (!(ok = slot_wait(use) && p_wait(t))) break;
-            product(t, use, i < 2);
-            tc_commit(smem_u32(&kv_empty[use % SLOTS]));
-            ++use;
-            if (i + 2 >= n) {
-              tc_commit(smem_u32(&o_done[t]));
-            } else {
-              if (!(ok = slot_wait(use))) break;
-              scores(t, use);
-              tc_commit(smem_u32(&kv_empty[use % SLOTS]));
-              ++use;
-            }
-          }
+          xattn_key_range(a.len, split, splits, j0, j1);
+          const uint32_t n = j1 - j0;
+          // the ring holds K0 K1 V0 K2 V1 K3 ..., this stream takes every second tile
+          if (static_cast<uint32_t>(t) < n && open(Next{true, static_cast<uint32_t>(t), true, false}))
+            for (uint32_t i = t; i < n; i += 2)
+              if (!advance(i + 1 < n ? 2 * i + 2 : 2 * n - 1, i < 2, Next{i + 2 < n, 2 * i + 3, false, false})) break;
         }
       } else {
-        // the tiles with keys, one ahead: a tile's first scores are issued
-        // behind the last product of the tile before
+        // the ring holds K0 V0 K1 V1 ... of the tiles with keys in turn
         auto next_tile = [&](int tile, int& n) -> int {
           for (; tile < p.tiles; tile += step) {
             int j0, j1;
-            key_range(xattn_tile(p, tile, kRows).len, j0, j1);
-            n = j1 - j0;
+            xattn_key_range(xattn_tile(p, tile, kRows).len, 0, 1, j0, j1);
+            n = j1;
             if (n > 0) break;
           }
           return tile;
         };
-        uint32_t count = 0;  // tiles with keys begun
         int n = 0;
         int tile = next_tile(first, n);
-        auto begin = [&](int t) -> bool {  // the first scores of the tile `count`, keys in slot `use`
-          if (!mbar_wait(smem_u32(&q_full[t]), count & 1, abort_flag, p.status) || !slot_wait(use)) return false;
-          scores(t, use);
-          return true;
-        };
-        if (tile < p.tiles) {
-          for (int t = 0; t < 2 && ok; ++t)
-            if ((ok = begin(t)) && n == 1) tc_commit(smem_u32(&q_empty[t]));
-          if (ok) tc_commit(smem_u32(&kv_empty[use % SLOTS]));
-          ++use;
-          ++count;
-        }
-        while (tile < p.tiles && ok) {
+        bool ok = tile < p.tiles && open(Next{true, 0u, true, n == 1});
+        uint32_t slot = 1;  // the next values
+        while (ok && tile < p.tiles) {
           int n_next = 0;
           const int tile_next = next_tile(tile + step, n_next);
-          for (int j = 0; j < n && ok; ++j) {
-            const uint32_t v = use, k = use + 1;
-            const bool more = j + 1 < n, follow = !more && tile_next < p.tiles;
-            for (int t = 0; t < 2 && ok; ++t) {
-              if (!(ok = slot_wait(v) && p_wait(t))) break;
-              product(t, v, j == 0);
-              if (t == 1) tc_commit(smem_u32(&kv_empty[v % SLOTS]));
-              if (!more) tc_commit(smem_u32(&o_done[t]));
-              if (more) {
-                if (!(ok = slot_wait(k))) break;
-                scores(t, k);
-                if (j + 2 == n) tc_commit(smem_u32(&q_empty[t]));
-              } else if (follow) {
-                use = k;
-                ok = begin(t);
-                use = v;
-                if (ok && n_next == 1) tc_commit(smem_u32(&q_empty[t]));
-              }
-              if (t == 1 && ok && (more || follow)) tc_commit(smem_u32(&kv_empty[k % SLOTS]));
-            }
-            use += (more || follow) ? 2 : 1;
-            if (follow) ++count;
+          for (int j = 0; ok && j < n; ++j, slot += 2) {
+            const bool more = j + 1 < n;
+            ok = advance(slot, j == 0,
+                         Next{more || tile_next < p.tiles, slot + 1, !more, more ? j + 2 == n : n_next == 1});
           }
           tile = tile_next;
           n = n_next;
         }
       }
-      tc_commit(smem_u32(drain));
-      mbar_wait_drain(smem_u32(drain), 0);
+      if (elect_one()) tc_commit(smem_u32(&drain[t]));
+      __syncwarp();
+      mbar_wait_drain(smem_u32(&drain[t]), 0);
     }
-  } else {
+  } else if (warp < 12) {
     // ------------------------------------------------------------ softmax: a row per thread
     regs_grow_to<kXRegsSoftmax>();
     const int t = (warp >> 2) - 1;  // stream
@@ -397,159 +438,165 @@ __global__ void __launch_bounds__(kXThreads, 1)
     const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
     const uint32_t t_s = tmem + 128 * t + lane_base, t_o = tmem + C::O_COL + 128 * t + lane_base;
     const float c = p.scale * 1.4426950408889634f;  // log2 e
-    uint32_t sc = 0, oc = 0;        // phases of s_full and o_done waited for
-    uint32_t fills = 0;             // ring fills of the tiles before
+    uint32_t it = 0;                // key tiles done
+    uint32_t fills = 0, closed = 0; // ring fills of the tiles before, tiles with keys done
     bool ok = true;
+    auto got = [&](uint64_t* bar, uint32_t parity) -> bool {
+      return mbar_wait_warp(smem_u32(bar), parity & 1, abort_flag, p.status);
+    };
     for (int tile = first; tile < p.tiles && ok; tile += step) {
       const XTileAt a = xattn_tile(p, tile, kRows);
       int j0, j1;
-      key_range(a.len, j0, j1);
+      xattn_key_range(a.len, split, splits, j0, j1);
       const int n = j1 - j0;
+      const bool some = SPLIT ? t < n : n > 0;  // this stream has keys here
       float m_used = -INFINITY, l = 0.0f;  // offset (log2 domain) and sum of 2^(c s - offset)
       bool begun = false;
-      for (int i = SPLIT ? t : 0; i < n; i += SPLIT ? 2 : 1) {
-        const int j = j0 + i;
-        // the keys of this tile that count, one bit each
-        uint32_t keep[4];
-        bool all = true;
+      // half key tiles (SPLIT: of every second key tile)
+      for (int u = SPLIT ? 2 * t : 0; u < 2 * n; u += SPLIT && (u & 1) ? 3 : 1) {
+        const int h = u & 1;
+        const int key0 = j0 * kXTile + u * kXSub;
+        // the keys of this half that count, one bit each
+        uint32_t keep[2];
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const int left = a.len - (j * kXTile + 32 * w);
+        for (int w = 0; w < 2; ++w) {
+          const int left = a.len - (key0 + 32 * w);
           keep[w] = left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1u;
           if (p.key_mask != nullptr) {
-            const int key = j * kXTile + 32 * w + lane;
+            const int key = key0 + 32 * w + lane;
             const bool on = key < p.Skv && p.key_mask[static_cast<int64_t>(a.kb) * p.ld_mask + key] != 0;
             keep[w] &= __ballot_sync(0xffffffffu, on);
           }
-          all = all && keep[w] == 0xffffffffu;
         }
-        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&s_full[t]), sc & 1, abort_flag, p.status))) {
+        const uint32_t t_buf = t_s + kXSub * h;
+        if (!got(&s_full[2 * t + h], it)) {
           ok = false;
           break;
         }
-        ++sc;
         tc_fence_after();
-        uint32_t sv[kXTile];
-#pragma unroll
-        for (int cc = 0; cc < kXTile / 32; ++cc)
-          tmem_ld_32cols(t_s + 32 * cc, *reinterpret_cast<uint32_t(*)[32]>(&sv[32 * cc]));
+        uint32_t sv[kXSub];
+        tmem_ld_32cols(t_buf, *reinterpret_cast<uint32_t(*)[32]>(&sv[0]));
+        tmem_ld_32cols(t_buf + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
         tmem_ld_wait();
-        if (!all) {
+        if ((keep[0] & keep[1]) != 0xffffffffu) {
           // Keys that do not count: no weight, and zeros for their values,
-          // which may hold anything (0 times NaN is NaN).  One of the streams
-          // that share a value tile clears them, once the tile has landed
-          // and before its probabilities let the product start.
+          // which may hold anything (0 times NaN is NaN): cleared once the
+          // tile has landed and before this stream's probabilities let its
+          // product start.  Streams that share a value tile both do it (the
+          // second writes zeros over zeros).
 #pragma unroll
-          for (int w = 0; w < 4; ++w)
-#pragma unroll
-            for (int b = 0; b < 32; ++b)
-              if (!(keep[w] >> b & 1)) sv[32 * w + b] = 0xff800000u;  // -inf
-          if (SPLIT || t == 0) {
-            const uint32_t v = SPLIT ? (i < n - 1 ? 2u * i + 2u : 2u * n - 1u) : fills + 2u * i + 1u;
-            if (!__all_sync(0xffffffffu,
-                            mbar_wait(smem_u32(&kv_full[v % SLOTS]), (v / SLOTS) & 1, abort_flag, p.status))) {
-              ok = false;
-              break;
-            }
-            const uint32_t mine = q == 0 ? keep[0] : q == 1 ? keep[1] : q == 2 ? keep[2] : keep[3];
-            if (!(mine >> lane & 1)) {
-              uint8_t* row = smem + C::KV_OFF + (v % SLOTS) * C::TILE_BYTES + r * 128;
-#pragma unroll
-              for (int d = 0; d < DB; ++d)
-#pragma unroll
-                for (int u = 0; u < 8; ++u)
-                  *reinterpret_cast<uint4*>(row + d * (kXTile * 128) + 16 * u) = make_uint4(0u, 0u, 0u, 0u);
-            }
-            fence_proxy_async_smem();
+          for (int e = 0; e < 32; ++e) {
+            if (!(keep[0] >> e & 1)) sv[e] = 0xff800000u;  // -inf
+            if (!(keep[1] >> e & 1)) sv[32 + e] = 0xff800000u;
           }
-        }
-        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          const uint32_t i = u >> 1;
+          const uint32_t v = SPLIT ? (i + 1 < static_cast<uint32_t>(n) ? 2 * i + 2 : 2 * n - 1) : fills + 2 * i + 1;
+          if (!got(&kv_full[v % SLOTS], v / SLOTS)) {
+            ok = false;
+            break;
+          }
+          // two threads a key, each half of its columns
+          if (!((q & 1 ? keep[1] : keep[0]) >> lane & 1)) {
+            uint8_t* row = smem + C::KV_OFF + (v % SLOTS) * C::TILE_BYTES + (kXSub * h + (r & 63)) * 128 +
+                           (r >> 6) * (DB == 2 ? kXTile * 128 : 64);
 #pragma unroll
-        for (int e = 0; e < kXTile; e += 2)
-          mx4[(e >> 1) & 3] = max3_nan(mx4[(e >> 1) & 3], __uint_as_float(sv[e]), __uint_as_float(sv[e + 1]));
-        const float m_tile = max3_nan(max3_nan(mx4[0], mx4[1], mx4[2]), mx4[3], mx4[3]) * c;
+            for (int e = 0; e < 4 * DB; ++e) *reinterpret_cast<uint4*>(row + 16 * e) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+        }
+        float mx[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          mx[e] = max3_nan(__uint_as_float(sv[e]), __uint_as_float(sv[e + 8]), __uint_as_float(sv[e + 16]));
+#pragma unroll
+        for (int e = 24; e < 56; e += 16)
+#pragma unroll
+          for (int w = 0; w < 8; ++w)
+            mx[w] = max3_nan(mx[w], __uint_as_float(sv[e + w]), __uint_as_float(sv[e + w + 8]));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) mx[e] = max3_nan(mx[e], __uint_as_float(sv[56 + e]), mx[e]);
+        const float m_tile =
+            max3_nan(max3_nan(mx[0], mx[1], mx[2]), max3_nan(mx[3], mx[4], mx[5]), max3_nan(mx[6], mx[7], mx[7])) * c;
         // a score that is NaN or +infinity makes its row NaN (the polynomial
         // below would drop it)
         if (!(m_tile < INFINITY)) l = __int_as_float(0x7fffffff);
         const bool moves = m_tile > m_used + kXSlack;
-        const float f = moves ? ex2_approx(m_used - m_tile) : 1.0f;
-        if (moves) {
-          m_used = m_tile;
-          l *= f;
-        }
-        if (begun && __any_sync(0xffffffffu, moves)) {
-          // (the scores' commit covers the product before them: O is at rest)
+        if (__any_sync(0xffffffffu, moves)) {
+          const float f = moves ? ex2_approx(m_used - m_tile) : 1.0f;
+          if (moves) {
+            m_used = m_tile;
+            l *= f;
+          }
+          if (begun) {
+            // O at rest: the half before is done when its buffer is full
+            // again (phase it + 1 of the first, phase it of the second)
+            if (!got(&s_full[2 * t + (h ^ 1)], h == 1 ? it + 1 : it)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
 #pragma unroll 1
-          for (int cc = 0; cc < DB * 4; ++cc) {
-            uint32_t v[16];
-            tmem_ld_16cols(t_o + 16 * cc, v);
-            tmem_ld_wait();
+            for (int cc = 0; cc < DB * 4; ++cc) {
+              uint32_t v[16];
+              tmem_ld_16cols(t_o + 16 * cc, v);
+              tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
-            tmem_st_16cols(t_o + 16 * cc, v);
+              for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
+              tmem_st_16cols(t_o + 16 * cc, v);
+            }
           }
         }
         begun = true;
         const float off = m_used == -INFINITY ? 0.0f : m_used;
-        float la = 0.0f, lb = 0.0f;
+        float la = 0.0f, lb = 0.0f, lc = 0.0f, ld = 0.0f;
+        uint32_t b[kXSub / 2];
 #pragma unroll
-        for (int cc = 0; cc < kXTile / 32; ++cc) {
-          uint32_t b[16];
+        for (int c0 = 0; c0 < kXSub; c0 += kXChunk) {
+          float y[kXChunk];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const uint32_t* v = &sv[32 * cc + 4 * e];
-            float x0, x1, x2, x3, p0, p1;
-            fma2_rn(x0, x1, __uint_as_float(v[0]), __uint_as_float(v[1]), c, c, -off, -off);
-            fma2_rn(x2, x3, __uint_as_float(v[2]), __uint_as_float(v[3]), c, c, -off, -off);
-            if ((e & 1) == 0) {  // one pair in four on the FMA pipes
-              exp2_poly2(p0, p1, x0, x1);
+          for (int e = 0; e < kXChunk; e += 2)
+            fma2_rn(y[e], y[e + 1], __uint_as_float(sv[c0 + e]), __uint_as_float(sv[c0 + e + 1]), c, c, -off, -off);
+#pragma unroll
+          for (int e = 0; e < kXChunk; e += 2) {
+            if (((c0 + e) >> 1) % 16 >= 16 - kXPolyPairs) {
+              exp2_poly2(y[e], y[e + 1], y[e], y[e + 1]);
             } else {
-              p0 = ex2_approx(x0);
-              p1 = ex2_approx(x1);
+              y[e] = ex2_approx(y[e]);
+              y[e + 1] = ex2_approx(y[e + 1]);
             }
-            const float p2 = ex2_approx(x2), p3 = ex2_approx(x3);
-            b[2 * e] = pack_bf16x2(p0, p1);
-            b[2 * e + 1] = pack_bf16x2(p2, p3);
-            float s0, s1;
-            add2_rn(s0, s1, p0, p1, p2, p3);
-            add2_rn(la, lb, la, lb, s0, s1);
           }
-          tmem_st_16cols(t_s + 16 * cc, b);
+#pragma unroll
+          for (int e = 0; e < kXChunk; e += 2) b[(c0 + e) / 2] = pack_bf16x2(y[e], y[e + 1]);
+#pragma unroll
+          for (int e = 0; e < kXChunk; e += 4) {
+            add2_rn(la, lb, la, lb, y[e], y[e + 1]);
+            add2_rn(lc, ld, lc, ld, y[e + 2], y[e + 3]);
+          }
+          if ((c0 + kXChunk) % 32 == 0)
+            tmem_st_16cols(t_buf + 16 * (c0 / 32), *reinterpret_cast<uint32_t(*)[16]>(&b[16 * (c0 / 32)]));
         }
-        l += la + lb;
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&p_full[t]));
+        if (lane == 0) mbar_arrive(smem_u32(&p_full[2 * t + h]));
+        l += (la + lc) + (lb + ld);
+        it += h;
       }
       if (!ok) break;
-      // ---------------------------------------------------------- epilogue
-      if (n > 0 && (!SPLIT || t < n)) {
-        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&o_done[t]), oc & 1, abort_flag, p.status))) {
-          ok = false;
-          break;
-        }
-        ++oc;
-        tc_fence_after();
-      }
       fills += 2u * n;
       if constexpr (SPLIT) {
-        // the other stream's products have read the ring too
-        if (t == 0 ? n > 1 : n > 0) {
-          if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&o_done[t ^ 1]), 0, abort_flag, p.status))) {
-            ok = false;
-            break;
-          }
-        }
-        float* stat = reinterpret_cast<float*>(smem + C::STAT_OFF);
-        stat[t * 2 * kXTile + r] = m_used;
-        stat[t * 2 * kXTile + kXTile + r] = l;
+        // both streams' last products are done, the ring is read
+        if ((some && !got(&o_done[t], 0)) || ((t == 0 ? n > 1 : n > 0) && !got(&o_done[t ^ 1], 0))) break;
+        tc_fence_after();
+        float* stat = reinterpret_cast<float*>(smem + C::STAT_OFF) + 2 * kXTile * t;
+        stat[r] = m_used;
+        stat[kXTile + r] = l;
         float* part = reinterpret_cast<float*>(smem) + (t * kXTile + r) * C::PART_PITCH;
         const bool live = a.row0 + r < p.Sq * p.pack;
 #pragma unroll 1
         for (int cc = 0; cc < DB * 4; ++cc) {
           uint32_t v[16];
-          if (t < n) {
+          if (some) {
             tmem_ld_16cols(t_o + 16 * cc, v);
             tmem_ld_wait();
           } else {
@@ -564,44 +611,82 @@ __global__ void __launch_bounds__(kXThreads, 1)
           }
         }
       } else {
-        const float f = n == 0 ? 0.0f : xattn_factor(m_used, l);
-        uint8_t* box = smem + C::O_OFF + (warp - 4) * (32 * 128);
+        if (!some) continue;
+        // the epilogue takes the sums over; it has read the factors of the
+        // tile before
+        if (closed > 0 && !got(&o_free[t], closed - 1)) break;
+        ++closed;
+        reinterpret_cast<float*>(smem + C::F_OFF)[t * kXTile + r] = xattn_factor(m_used, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&f_full[t]));
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue: a row per thread
+    regs_release_to<kXRegsEpi>();
+    const int q = warp & 3;  // TMEM lane quarter
+    const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
+    uint8_t* boxes = smem + C::O_OFF + q * (2 * 32 * 128);
+    uint32_t closed = 0, stores = 0;  // tiles with keys done; boxes filled
+    bool ok = !SPLIT;
+    for (int tile = first; tile < p.tiles && ok; tile += step) {
+      const XTileAt a = xattn_tile(p, tile, kRows);
+      const bool some = a.len > 0;
+      for (int t = 0; t < 2 && ok; ++t) {
+        float f = 0.0f;
+        if (some) {
+          if (!mbar_wait_warp(smem_u32(&f_full[t]), closed & 1, abort_flag, p.status) ||
+              !mbar_wait_warp(smem_u32(&o_done[t]), closed & 1, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          f = reinterpret_cast<const float*>(smem + C::F_OFF)[t * kXTile + q * 32 + lane];
+        }
+        // the row's sums out of TMEM at once, so that the next tile's first
+        // product can overwrite them
+        uint32_t b[DB * 32];
+#pragma unroll
+        for (int hh = 0; hh < DB * 2; ++hh) {
+          uint32_t v[32];
+          if (some) {
+            tmem_ld_32cols(tmem + C::O_COL + 128 * t + lane_base + 32 * hh, v);
+            tmem_ld_wait();
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = 0u;
+          }
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float o0, o1;
+            mul2_rn(o0, o1, __uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]), f, f);
+            b[16 * hh + e] = pack_bf16x2(o0, o1);
+          }
+        }
+        if (some) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&o_free[t]));
+        }
         const int tok0 = (a.row0 + t * kXTile + q * 32) / p.pack;
-#pragma unroll 1
-        for (int d = 0; d < DB; ++d) {
-          if (lane == 0) bulk_wait_group_read<0>();  // the box's last store has been read
+#pragma unroll
+        for (int d = 0; d < DB; ++d, ++stores) {
+          uint8_t* box = boxes + (stores & 1) * (32 * 128);
+          if (lane == 0) bulk_wait_group_read<1>();  // the store before the last has read this box
           __syncwarp();
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            uint32_t v[32];
-            if (n > 0) {
-              tmem_ld_32cols(t_o + 64 * d + 32 * hh, v);
-              tmem_ld_wait();
-            } else {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] = 0u;
-            }
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              uint4 w;
-              w.x = pack_bf16x2(__uint_as_float(v[8 * u]) * f, __uint_as_float(v[8 * u + 1]) * f);
-              w.y = pack_bf16x2(__uint_as_float(v[8 * u + 2]) * f, __uint_as_float(v[8 * u + 3]) * f);
-              w.z = pack_bf16x2(__uint_as_float(v[8 * u + 4]) * f, __uint_as_float(v[8 * u + 5]) * f);
-              w.w = pack_bf16x2(__uint_as_float(v[8 * u + 6]) * f, __uint_as_float(v[8 * u + 7]) * f);
-              *reinterpret_cast<uint4*>(box + lane * 128 + (((4 * hh + u) ^ (lane & 7)) << 4)) = w;
-            }
-          }
+          for (int u = 0; u < 8; ++u)
+            *reinterpret_cast<uint4*>(box + lane * 128 + ((u ^ (lane & 7)) << 4)) =
+                make_uint4(b[32 * d + 4 * u], b[32 * d + 4 * u + 1], b[32 * d + 4 * u + 2], b[32 * d + 4 * u + 3]);
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0 && tok0 < p.Sq) {
-            tma_store_4d(&tm_o, smem_u32(box), 64 * d, a.h0, tok0, a.b);
+          if (lane == 0) {
+            if (tok0 < p.Sq) tma_store_4d(&tm_o, smem_u32(box), 64 * d, a.h0, tok0, a.b);
             bulk_commit_group();
           }
         }
-        // (O is read: the next tile's first product waits for this thread's
-        // next probabilities)
-        tc_fence_before();
       }
+      if (some) ++closed;
     }
     if (!SPLIT && lane == 0) bulk_wait_group_all();
     __syncwarp();
@@ -609,7 +694,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
 
   if constexpr (SPLIT) {
     cluster_sync();  // every CTA's partial sums are in its shared memory
-    if (warp >= 4 && first < p.tiles && *abort_flag == 0) {
+    if (warp >= 4 && warp < 12 && first < p.tiles && *abort_flag == 0) {
       // rows of the tile times groups of four columns, shared out over the cluster
       const XTileAt a = xattn_tile(p, first, kRows);
       const int rows = min(kXTile, p.Sq * p.pack - a.row0), groups = p.D / 4;
