@@ -42,7 +42,7 @@ constexpr int kXThreads = 512;    // control warpgroup, a softmax warpgroup a st
 constexpr float kXSlack = 8.0f;   // binades a tile's maximum may pass the offset
 constexpr int kXChunk = 16;       // scores taken together through the exponential
 constexpr int kXPolyPairs = 2;    // of 16 pairs of exponentials, how many on the FMA pipes instead of the MUFU
-constexpr int kXRegsCtrl = 64, kXRegsSoftmax = 168, kXRegsEpi = 112;  // of 128 at launch
+constexpr int kXRegsCtrl = 80, kXRegsSoftmax = 160, kXRegsEpi = 112;  // of 128 at launch
 static_assert(128 * (kXRegsCtrl + kXRegsEpi) + 256 * kXRegsSoftmax <= kXThreads * 128,
               "register budgets fit the launch allocation");
 
@@ -52,6 +52,9 @@ struct XAttnParams {
   int batch, kv_batch;
   int row_tiles;            // work tiles along the queries (128 or 256 rows each)
   int tiles;                // work tiles in all
+  int head_blocks;          // heads / pack
+  int step, step_rt, step_hb, step_b;  // tiles from one of a CTA's to its next, and the same as a decoded tile
+  uint32_t hb_magic;        // hb / (head blocks of a key/value head) = umulhi(hb, hb_magic); 0 for a divisor of 1
   const int* kv_len;        // [kv_batch] or nullptr
   const uint8_t* key_mask;  // [kv_batch, ld_mask] or nullptr; 0: not attended to
   int64_t ld_mask;
@@ -131,20 +134,63 @@ struct XTileAt {
   int len;   // keys
 };
 
-__device__ __forceinline__ XTileAt xattn_tile(const XAttnParams& p, int tile, int rows) {
-  XTileAt a;
-  const int blocks = p.heads / p.pack;
-  const int rt = tile % p.row_tiles;
-  const int hb = (tile / p.row_tiles) % blocks;
-  a.b = tile / (p.row_tiles * blocks);
-  a.row0 = rt * rows;
-  a.h0 = hb * p.pack;
-  a.hk = a.h0 / (p.heads / p.kv_heads);
-  a.kb = p.kv_batch == 1 ? 0 : a.b;
-  a.len = p.Skv;
-  if (p.kv_len != nullptr) a.len = min(max(p.kv_len[a.kb], 0), p.Skv);
-  return a;
-}
+// A role's walk over a CTA's work tiles, gridDim.x apart in the persistent
+// form.  Only the first is decoded by division; each tile's key length is
+// loaded a tile ahead (decoding a tile afresh and loading its length took 3500
+// cycles of every softmax warp, as long as two and a half key halves).
+struct XWalk {
+  int tile, rt, hb, b;  // work tile: row tile, head block, sequence
+  int len, len1;        // its key length as loaded, and that of the tile behind
+
+  __device__ __forceinline__ int load(const XAttnParams& p, int seq) const {
+    return p.kv_len != nullptr && seq < p.batch ? p.kv_len[p.kv_batch == 1 ? 0 : seq] : p.Skv;
+  }
+  // (row tile, head block, sequence) of the tile behind
+  __device__ __forceinline__ void behind(const XAttnParams& p, int& rt1, int& hb1, int& b1) const {
+    rt1 = rt + p.step_rt;
+    hb1 = hb + p.step_hb;
+    b1 = b + p.step_b;
+    if (rt1 >= p.row_tiles) {
+      rt1 -= p.row_tiles;
+      ++hb1;
+    }
+    if (hb1 >= p.head_blocks) {
+      hb1 -= p.head_blocks;
+      ++b1;
+    }
+  }
+  __device__ __forceinline__ void look_ahead(const XAttnParams& p) {
+    int rt1, hb1, b1;
+    behind(p, rt1, hb1, b1);
+    len1 = load(p, b1);
+  }
+  __device__ __forceinline__ XWalk(const XAttnParams& p, int first) : tile(first) {
+    rt = first % p.row_tiles;
+    const int heads = first / p.row_tiles;
+    hb = heads % p.head_blocks;
+    b = heads / p.head_blocks;
+    len = load(p, b);
+    look_ahead(p);
+  }
+  __device__ __forceinline__ bool live(const XAttnParams& p) const { return tile < p.tiles; }
+  __device__ __forceinline__ void next(const XAttnParams& p) {
+    behind(p, rt, hb, b);
+    tile += p.step;
+    len = len1;
+    look_ahead(p);
+  }
+  __device__ __forceinline__ int keys(const XAttnParams& p) const { return min(max(len, 0), p.Skv); }
+  __device__ __forceinline__ XTileAt at(const XAttnParams& p, int rows) const {
+    XTileAt a;
+    a.row0 = rt * rows;
+    a.h0 = hb * p.pack;
+    a.hk = static_cast<int>(p.hb_magic != 0 ? __umulhi(static_cast<uint32_t>(hb), p.hb_magic) : static_cast<uint32_t>(hb));
+    a.b = b;
+    a.kb = p.kv_batch == 1 ? 0 : b;
+    a.len = keys(p);
+    return a;
+  }
+};
 
 // Key tiles [j0, j1) of `len` keys that fall to one of `splits` CTAs.
 __device__ __forceinline__ void xattn_key_range(int len, int split, int splits, int& j0, int& j1) {
@@ -224,7 +270,6 @@ __global__ void __launch_bounds__(kXThreads, 1)
   const int splits = SPLIT ? static_cast<int>(gridDim.x) : 1;
   const int split = SPLIT ? static_cast<int>(blockIdx.x) : 0;
   const int first = SPLIT ? static_cast<int>(blockIdx.y) : static_cast<int>(blockIdx.x);
-  const int step = SPLIT ? p.tiles : static_cast<int>(gridDim.x);
 
   if (warp < 4) {
     regs_release_to<kXRegsCtrl>();
@@ -243,8 +288,8 @@ __global__ void __launch_bounds__(kXThreads, 1)
                       j * kXTile, a.kb);
         ++fill;
       };
-      for (int tile = first; tile < p.tiles && ok; tile += step) {
-        const XTileAt a = xattn_tile(p, tile, kRows);
+      for (XWalk w(p, first); w.live(p) && ok; w.next(p)) {
+        const XTileAt a = w.at(p, kRows);
         int j0, j1;
         xattn_key_range(a.len, split, splits, j0, j1);
         if (SPLIT) {
@@ -269,8 +314,8 @@ __global__ void __launch_bounds__(kXThreads, 1)
       // work tile before, and would hold up the keys and values behind it)
       uint32_t fills[2] = {0u, 0u};
       bool ok = true;
-      for (int tile = first; tile < p.tiles && ok; tile += step) {
-        const XTileAt a = xattn_tile(p, tile, kRows);
+      for (XWalk w(p, first); w.live(p) && ok; w.next(p)) {
+        const XTileAt a = w.at(p, kRows);
         int j0, j1;
         xattn_key_range(a.len, split, splits, j0, j1);
         if (j0 == j1) continue;
@@ -285,13 +330,15 @@ __global__ void __launch_bounds__(kXThreads, 1)
                         (a.row0 + t * kXTile) / p.pack, a.b);
           ++fills[t];
         }
-        if (!SPLIT && tile + step < p.tiles) {
+        if (!SPLIT && w.tile + p.step < p.tiles) {
           // the next tile's towards L2 meanwhile
-          const XTileAt z = xattn_tile(p, tile + step, kRows);
-          for (int t = 0; t < 2; ++t)
-            if ((z.row0 + t * kXTile) / p.pack < p.Sq)
-              for (int d = 0; d < DB; ++d)
-                tma_prefetch_4d(&tm_q, 64 * d, z.h0, (z.row0 + t * kXTile) / p.pack, z.b);
+          int rt1, hb1, b1;
+          w.behind(p, rt1, hb1, b1);
+          for (int t = 0; t < 2; ++t) {
+            const int token = (rt1 * kRows + t * kXTile) / p.pack;
+            if (token < p.Sq)
+              for (int d = 0; d < DB; ++d) tma_prefetch_4d(&tm_q, 64 * d, hb1 * p.pack, token, b1);
+          }
         }
       }
 #pragma unroll
@@ -388,10 +435,10 @@ __global__ void __launch_bounds__(kXThreads, 1)
         return true;
       };
       if (SPLIT) {
-        if (first < p.tiles) {
-          const XTileAt a = xattn_tile(p, first, kRows);
+        const XWalk w(p, first);
+        if (w.live(p)) {
           int j0, j1;
-          xattn_key_range(a.len, split, splits, j0, j1);
+          xattn_key_range(w.keys(p), split, splits, j0, j1);
           const uint32_t n = j1 - j0;
           // the ring holds K0 K1 V0 K2 V1 K3 ..., this stream takes every second tile
           if (static_cast<uint32_t>(t) < n && open(Next{true, static_cast<uint32_t>(t), true, false}))
@@ -400,28 +447,21 @@ __global__ void __launch_bounds__(kXThreads, 1)
         }
       } else {
         // the ring holds K0 V0 K1 V1 ... of the tiles with keys in turn
-        auto next_tile = [&](int tile, int& n) -> int {
-          for (; tile < p.tiles; tile += step) {
-            int j0, j1;
-            xattn_key_range(xattn_tile(p, tile, kRows).len, 0, 1, j0, j1);
-            n = j1;
-            if (n > 0) break;
-          }
-          return tile;
+        XWalk w(p, first);  // stands on the tile behind
+        auto next_keys = [&]() -> int {  // key tiles of the next tile with keys, 0: none
+          int n = 0;
+          for (; n == 0 && w.live(p); w.next(p)) n = (w.keys(p) + kXTile - 1) / kXTile;
+          return n;
         };
-        int n = 0;
-        int tile = next_tile(first, n);
-        bool ok = tile < p.tiles && open(Next{true, 0u, true, n == 1});
+        int n = next_keys();
+        bool ok = n > 0 && open(Next{true, 0u, true, n == 1});
         uint32_t slot = 1;  // the next values
-        while (ok && tile < p.tiles) {
-          int n_next = 0;
-          const int tile_next = next_tile(tile + step, n_next);
+        while (ok && n > 0) {
+          const int n_next = next_keys();
           for (int j = 0; ok && j < n; ++j, slot += 2) {
             const bool more = j + 1 < n;
-            ok = advance(slot, j == 0,
-                         Next{more || tile_next < p.tiles, slot + 1, !more, more ? j + 2 == n : n_next == 1});
+            ok = advance(slot, j == 0, Next{more || n_next > 0, slot + 1, !more, more ? j + 2 == n : n_next == 1});
           }
-          tile = tile_next;
           n = n_next;
         }
       }
@@ -444,8 +484,8 @@ __global__ void __launch_bounds__(kXThreads, 1)
     auto got = [&](uint64_t* bar, uint32_t parity) -> bool {
       return mbar_wait_warp(smem_u32(bar), parity & 1, abort_flag, p.status);
     };
-    for (int tile = first; tile < p.tiles && ok; tile += step) {
-      const XTileAt a = xattn_tile(p, tile, kRows);
+    for (XWalk w(p, first); w.live(p) && ok; w.next(p)) {
+      const XTileAt a = w.at(p, kRows);
       int j0, j1;
       xattn_key_range(a.len, split, splits, j0, j1);
       const int n = j1 - j0;
@@ -459,13 +499,13 @@ __global__ void __launch_bounds__(kXThreads, 1)
         // the keys of this half that count, one bit each
         uint32_t keep[2];
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          const int left = a.len - (key0 + 32 * w);
-          keep[w] = left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1u;
+        for (int w32 = 0; w32 < 2; ++w32) {
+          const int left = a.len - (key0 + 32 * w32);
+          keep[w32] = left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1u;
           if (p.key_mask != nullptr) {
-            const int key = key0 + 32 * w + lane;
+            const int key = key0 + 32 * w32 + lane;
             const bool on = key < p.Skv && p.key_mask[static_cast<int64_t>(a.kb) * p.ld_mask + key] != 0;
-            keep[w] &= __ballot_sync(0xffffffffu, on);
+            keep[w32] &= __ballot_sync(0xffffffffu, on);
           }
         }
         const uint32_t t_buf = t_s + kXSub * h;
@@ -479,30 +519,45 @@ __global__ void __launch_bounds__(kXThreads, 1)
         tmem_ld_32cols(t_buf + 32, *reinterpret_cast<uint32_t(*)[32]>(&sv[32]));
         tmem_ld_wait();
         if ((keep[0] & keep[1]) != 0xffffffffu) {
-          // Keys that do not count: no weight, and zeros for their values,
-          // which may hold anything (0 times NaN is NaN): cleared once the
-          // tile has landed and before this stream's probabilities let its
-          // product start.  Streams that share a value tile both do it (the
-          // second writes zeros over zeros).
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            if (!(keep[0] >> e & 1)) sv[e] = 0xff800000u;  // -inf
-            if (!(keep[1] >> e & 1)) sv[32 + e] = 0xff800000u;
-          }
+          // The values of keys that do not count may hold anything (0 times
+          // NaN is NaN): cleared once the tile has landed and before this
+          // stream's probabilities let its product start.  Streams that
+          // share a value tile both do it (the second writes zeros over
+          // zeros).
           const uint32_t i = u >> 1;
           const uint32_t v = SPLIT ? (i + 1 < static_cast<uint32_t>(n) ? 2 * i + 2 : 2 * n - 1) : fills + 2 * i + 1;
           if (!got(&kv_full[v % SLOTS], v / SLOTS)) {
             ok = false;
             break;
           }
-          // two threads a key, each half of its columns
+          // two threads a key, each half of its columns (in an order that
+          // spreads the lanes' rows over the banks)
           if (!((q & 1 ? keep[1] : keep[0]) >> lane & 1)) {
             uint8_t* row = smem + C::KV_OFF + (v % SLOTS) * C::TILE_BYTES + (kXSub * h + (r & 63)) * 128 +
                            (r >> 6) * (DB == 2 ? kXTile * 128 : 64);
 #pragma unroll
-            for (int e = 0; e < 4 * DB; ++e) *reinterpret_cast<uint4*>(row + 16 * e) = make_uint4(0u, 0u, 0u, 0u);
+            for (int e = 0; e < 4 * DB; ++e)
+              *reinterpret_cast<uint4*>(row + 16 * ((e ^ lane) & (4 * DB - 1))) = make_uint4(0u, 0u, 0u, 0u);
           }
           fence_proxy_async_smem();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            if (!(keep[0] >> e & 1)) sv[e] = 0xff800000u;  // -inf: no weight
+            if (!(keep[1] >> e & 1)) sv[32 + e] = 0xff800000u;
+          }
+          if ((keep[0] | keep[1]) == 0u) {
+            // no key of this half counts: no probabilities, nothing to sum
+            const uint32_t zero[16] = {};
+            tmem_st_16cols(t_buf, zero);
+            tmem_st_16cols(t_buf + 16, zero);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&p_full[2 * t + h]));
+            begun = true;
+            it += h;
+            continue;
+          }
         }
         float mx[8];
 #pragma unroll
@@ -629,8 +684,8 @@ __global__ void __launch_bounds__(kXThreads, 1)
     uint8_t* boxes = smem + C::O_OFF + q * (2 * 32 * 128);
     uint32_t closed = 0, stores = 0;  // tiles with keys done; boxes filled
     bool ok = !SPLIT;
-    for (int tile = first; tile < p.tiles && ok; tile += step) {
-      const XTileAt a = xattn_tile(p, tile, kRows);
+    for (XWalk w(p, first); w.live(p) && ok; w.next(p)) {
+      const XTileAt a = w.at(p, kRows);
       const bool some = a.len > 0;
       for (int t = 0; t < 2 && ok; ++t) {
         float f = 0.0f;
@@ -696,7 +751,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
     cluster_sync();  // every CTA's partial sums are in its shared memory
     if (warp >= 4 && warp < 12 && first < p.tiles && *abort_flag == 0) {
       // rows of the tile times groups of four columns, shared out over the cluster
-      const XTileAt a = xattn_tile(p, first, kRows);
+      const XTileAt a = XWalk(p, first).at(p, kRows);
       const int rows = min(kXTile, p.Sq * p.pack - a.row0), groups = p.D / 4;
       const uint32_t part0 = smem_u32(smem), stat0 = smem_u32(smem + C::STAT_OFF);
       for (int e = split * 256 + threadIdx.x - 128; e < rows * groups; e += splits * 256) {

@@ -829,10 +829,20 @@ int launch_cross_attention(const void* Q, int64_t ldq, const void* K, int64_t ld
       !encode_heads(&to, p.O, p.D, p.heads, p.Sq, p.batch, p.ldo, pack, 32 / pack))
     return W4A4_ERR_CUDA;
   p.row_tiles = static_cast<int>(ceil_div(static_cast<int64_t>(p.Sq) * p.pack, C::SPLIT ? kXTile : 2 * kXTile));
-  p.tiles = p.row_tiles * (p.heads / p.pack) * p.batch;
+  p.head_blocks = p.heads / p.pack;
+  p.tiles = p.row_tiles * p.head_blocks * p.batch;
+  // head blocks of a key/value head: division by multiplication, exact while
+  // both are below 2^16 (ceil(2^32 / d) n is less than n d / 2^32 < 1 too large)
+  const uint32_t per_kv = static_cast<uint32_t>(p.head_blocks / p.kv_heads);
+  p.hb_magic = per_kv == 1 ? 0u : static_cast<uint32_t>(((uint64_t(1) << 32) + per_kv - 1) / per_kv);
+  const int ctas = std::min(p.tiles, dev->num_sms);
+  p.step = C::SPLIT ? p.tiles : ctas;
+  p.step_rt = p.step % p.row_tiles;
+  p.step_hb = p.step / p.row_tiles % p.head_blocks;
+  p.step_b = p.step / p.row_tiles / p.head_blocks;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = C::SPLIT ? dim3(static_cast<unsigned>(splits), static_cast<unsigned>(p.tiles), 1)
-                         : dim3(static_cast<unsigned>(std::min(p.tiles, dev->num_sms)), 1, 1);
+                         : dim3(static_cast<unsigned>(ctas), 1, 1);
   cfg.blockDim = dim3(kXThreads, 1, 1);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = stream;
