@@ -111,20 +111,6 @@ __device__ __forceinline__ float xattn_factor(float m, float l) {
   return m == -INFINITY && l == l ? 0.0f : 1.0f / l;
 }
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
-
 // What a work tile index stands for.
 struct XTileAt {
   int row0;  // first row (token-major, `pack` heads a token) of the tile's first stream
@@ -756,22 +742,43 @@ __global__ void __launch_bounds__(kXThreads, 1)
       const uint32_t part0 = smem_u32(smem), stat0 = smem_u32(smem + C::STAT_OFF);
       for (int e = split * 256 + threadIdx.x - 128; e < rows * groups; e += splits * 256) {
         const int row = e / groups, g = e % groups;
-        float m = -INFINITY;
-        for (int s = 0; s < 2 * splits; ++s)
-          m = fmaxf(m, ld_cluster_f32(mapa_shared(stat0 + 4u * ((s & 1) * 2 * kXTile + row), s >> 1)));
+        // every stream of every CTA: all offsets, then sums and columns, asked
+        // for before the first is used
+        float ms[16], m = -INFINITY;
+#pragma unroll
+        for (int s = 0; s < 16; ++s)
+          ms[s] = s < 2 * splits
+                      ? ld_cluster_f32(mapa_shared(stat0 + 4u * ((s & 1) * 2 * kXTile + row), s >> 1))
+                      : -INFINITY;
+#pragma unroll
+        for (int s = 0; s < 16; ++s) m = fmaxf(m, ms[s]);
         float l = 0.0f;
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int s = 0; s < 2 * splits; ++s) {
-          const uint32_t st = mapa_shared(stat0 + 4u * ((s & 1) * 2 * kXTile + row), s >> 1);
-          const float ms = ld_cluster_f32(st);
-          const float w = ms == m ? 1.0f : ex2_approx(ms - m);
-          l = fmaf(w, ld_cluster_f32(st + 4u * kXTile), l);
-          const float4 v =
-              ld_cluster_f32x4(mapa_shared(part0 + 4u * (((s & 1) * kXTile + row) * C::PART_PITCH + 4 * g), s >> 1));
-          o.x = fmaf(w, v.x, o.x);
-          o.y = fmaf(w, v.y, o.y);
-          o.z = fmaf(w, v.z, o.z);
-          o.w = fmaf(w, v.w, o.w);
+#pragma unroll
+        for (int s0 = 0; s0 < 16; s0 += 8) {
+          if (s0 >= 2 * splits) break;
+          float ls[8];
+          float4 v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int s = s0 + i;
+            ls[i] = 0.0f;
+            v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (s < 2 * splits) {
+              ls[i] = ld_cluster_f32(mapa_shared(stat0 + 4u * ((s & 1) * 2 * kXTile + kXTile + row), s >> 1));
+              v[i] = ld_cluster_f32x4(
+                  mapa_shared(part0 + 4u * (((s & 1) * kXTile + row) * C::PART_PITCH + 4 * g), s >> 1));
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float w = ms[s0 + i] == m ? 1.0f : ex2_approx(ms[s0 + i] - m);
+            l = fmaf(w, ls[i], l);
+            o.x = fmaf(w, v[i].x, o.x);
+            o.y = fmaf(w, v[i].y, o.y);
+            o.z = fmaf(w, v[i].z, o.z);
+            o.w = fmaf(w, v[i].w, o.w);
+          }
         }
         const float f = xattn_factor(m, l);
         const int token = (a.row0 + row) / p.pack, head = a.h0 + (a.row0 + row) % p.pack;

@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // (warp: uniform)
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
 
@@ -156,30 +156,36 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (even CTA)
-    if (leader && lane == 0) {
+    // (the whole warp in uniform control flow, one elected lane issuing)
+    if (leader) {
       constexpr uint32_t kIdesc = idesc_e4m3(256, BN);
+      const uint64_t a_desc = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
+      const uint64_t w_desc = smem_desc(smem_u32(smem + C::A_BYTES), 16, 1024, kSwizzle128B);
       uint32_t it = 0, tcount = 0;
-      for (int tile = pair; tile < total; tile += pairs, ++tcount) {
+      bool ok = true;
+      for (int tile = pair; tile < total && ok; tile += pairs, ++tcount) {
         const uint32_t acc = tcount % C::NUM_ACC;
-        if (!mbar_wait(smem_u32(&acc_empty[acc]), ((tcount / C::NUM_ACC) & 1) ^ 1, abort_flag, p.status)) break;
+        if (!(ok = mbar_wait_warp(smem_u32(&acc_empty[acc]), ((tcount / C::NUM_ACC) & 1) ^ 1, abort_flag, p.status)))
+          break;
         tc_fence_after();
         const uint32_t d = tmem + acc * BN;
-        bool ok = true;
         for (int kb = 0; kb < nkb; ++kb, ++it) {
-          const int s = it % STAGES;
-          if (!mbar_wait(smem_u32(&full[s]), (it / STAGES) & 1, abort_flag, p.status)) { ok = false; break; }
+          const uint32_t s = it % STAGES;
+          if (!(ok = mbar_wait_warp(smem_u32(&full[s]), (it / STAGES) & 1, abort_flag, p.status))) break;
           tc_fence_after();
-          const uint32_t a_base = smem_u32(smem + s * C::STAGE_BYTES), w_base = a_base + C::A_BYTES;
+          const uint64_t ad = a_desc + s * (C::STAGE_BYTES >> 4), wd = w_desc + s * (C::STAGE_BYTES >> 4);
+          if (elect_one()) {
 #pragma unroll
-          for (int j = 0; j < C::BK / 32; ++j)
-            mma_e4m3_pair(d, smem_desc(a_base + 32 * j, 16, 1024, kSwizzle128B),
-                          smem_desc(w_base + 32 * j, 16, 1024, kSwizzle128B), kIdesc, (kb > 0 || j > 0) ? 1u : 0u);
-          tc_commit_pair_mc(smem_u32(&empty[s]), 0x3);
+            for (int j = 0; j < C::BK / 32; ++j)
+              mma_e4m3_pair(d, ad + (32 * j >> 4), wd + (32 * j >> 4), kIdesc, (kb > 0 || j > 0) ? 1u : 0u);
+            tc_commit_pair_mc(smem_u32(&empty[s]), 0x3);
+            if (kb == nkb - 1) tc_commit_pair_mc(smem_u32(&acc_full[acc]), 0x3);
+          }
+          __syncwarp();
         }
-        if (!ok) break;
-        tc_commit_pair_mc(smem_u32(&acc_full[acc]), 0x3);
       }
-      tc_commit_pair(smem_u32(drain));
+      if (elect_one()) tc_commit_pair(smem_u32(drain));
+      __syncwarp();
       mbar_wait_drain(smem_u32(drain), 0);
     }
   } else if (warp >= C::EPI_WARP0) {
@@ -342,7 +348,7 @@ __global__ void __launch_bounds__(C::THREADS, 2)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // (warp: uniform)
   const int splits = gridDim.x;               // the cluster spans the K slices of one weight tile
   const int split = blockIdx.x;
   const int n0 = blockIdx.y * C::BM;
@@ -386,20 +392,24 @@ __global__ void __launch_bounds__(C::THREADS, 2)
       tma_load_2d(smem_u32(st + C::W_BYTES), &tm_x, bar, (k0 + it) * C::BK, 0);
     }
     for (int j = max(0, it - STAGES); j < it; ++j) mbar_wait_drain(smem_u32(&full[j % STAGES]), (j / STAGES) & 1);
-  } else if (warp == 1 && lane == 0) {
+  } else if (warp == 1) {
     constexpr uint32_t kIdesc = idesc_e4m3(C::BM, C::TN);
+    const uint64_t w_desc = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
+    const uint64_t x_desc = smem_desc(smem_u32(smem + C::W_BYTES), 16, 1024, kSwizzle128B);
     for (int it = 0; it < steps; ++it) {
-      const int s = it % STAGES;
-      if (!mbar_wait(smem_u32(&full[s]), (it / STAGES) & 1, abort_flag, p.status)) break;
+      const uint32_t s = it % STAGES;
+      if (!mbar_wait_warp(smem_u32(&full[s]), (it / STAGES) & 1, abort_flag, p.status)) break;
       tc_fence_after();
-      const uint32_t w_base = smem_u32(smem + s * C::STAGE_BYTES), x_base = w_base + C::W_BYTES;
+      const uint64_t wd = w_desc + s * (C::STAGE_BYTES >> 4), xd = x_desc + s * (C::STAGE_BYTES >> 4);
+      if (elect_one()) {
 #pragma unroll
-      for (int j = 0; j < C::BK / 32; ++j)
-        mma_e4m3(tmem, smem_desc(w_base + 32 * j, 16, 1024, kSwizzle128B),
-                 smem_desc(x_base + 32 * j, 16, 1024, kSwizzle128B), kIdesc, (it > 0 || j > 0) ? 1u : 0u);
-      tc_commit(smem_u32(&empty[s]));
+        for (int j = 0; j < C::BK / 32; ++j)
+          mma_e4m3(tmem, wd + (32 * j >> 4), xd + (32 * j >> 4), kIdesc, (it > 0 || j > 0) ? 1u : 0u);
+        tc_commit(smem_u32(&empty[s]));
+      }
+      __syncwarp();
     }
-    tc_commit(smem_u32(done));  // completes once every MMA above has, abort or not
+    if (elect_one()) tc_commit(smem_u32(done));  // completes once every MMA above has, abort or not
   }
   __syncwarp();
   const bool ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(done), 0, abort_flag, p.status));
@@ -418,25 +428,56 @@ __global__ void __launch_bounds__(C::THREADS, 2)
     for (int j = 0; j < 16; ++j) part[(c + j) * C::BM + row] = ok ? __uint_as_float(r[j]) : 0.0f;
   }
   cluster_sync();
-  const int n = n0 + row;
-  if (ok && n < p.N) {
-    const float sw = __ldg(p.s_w + n);
-    const float b = p.bias != nullptr ? __bfloat162float(p.bias[n]) : 0.0f;
-    const uint32_t mine = smem_u32(part + row);
-    for (int m = split; m < p.M; m += splits) {
-      float acc = 0.0f;
-      for (int s = 0; s < splits; ++s) {
-        float v;
-        asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                     : "=f"(v)
-                     : "r"(mapa_shared(mine + static_cast<uint32_t>(m) * C::BM * 4, static_cast<uint32_t>(s)))
-                     : "memory");
-        acc += v;
+  // Outputs: a token per warp, four weight rows a lane.  Two tokens at a time,
+  // all their partial sums asked for before the first is added (one load
+  // after the other, a row a thread, took 128 tokens 12 us).
+  const int n = n0 + 4 * lane;
+  if (ok && n < p.N) {  // N % 8 == 0: all four are valid
+    const float4 sw = __ldg(reinterpret_cast<const float4*>(p.s_w + n));
+    uint2 bw = make_uint2(0u, 0u);
+    if (p.bias != nullptr) bw = __ldg(reinterpret_cast<const uint2*>(p.bias + n));
+    const uint32_t mine = smem_u32(part + 4 * lane);
+    const int stride = 4 * splits;  // tokens from one of a warp's to its next
+    for (int m0 = split + warp * splits; m0 < p.M; m0 += 2 * stride) {
+      float4 v[2][8];
+      float sa[2];
+      uint2 res[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int m = m0 + i * stride;
+        const bool on = m < p.M;
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+          v[i][s] = on && s < splits ? ld_cluster_f32x4(mapa_shared(mine + static_cast<uint32_t>(m) * C::BM * 4,
+                                                                    static_cast<uint32_t>(s)))
+                                     : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        sa[i] = on ? __ldg(p.s_a + static_cast<int64_t>(m) * p.s_a_step) : 0.0f;
+        // (a plain load: Y may be the residual itself)
+        res[i] = on && p.R != nullptr ? *reinterpret_cast<const uint2*>(p.R + static_cast<int64_t>(m) * p.ldr + n)
+                                      : make_uint2(0u, 0u);
       }
-      float y = fmaf(acc * __ldg(p.s_a + static_cast<int64_t>(m) * p.s_a_step), sw, b);
-      if (p.epi == 1) y = gelu_tanh_f32(y);
-      if (p.R != nullptr) y += __bfloat162float(p.R[static_cast<int64_t>(m) * p.ldr + n]);
-      p.Y[static_cast<int64_t>(m) * p.ldy + n] = __float2bfloat16_rn(y);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int m = m0 + i * stride;
+        if (m >= p.M) break;
+        float4 acc = v[i][0];
+#pragma unroll
+        for (int s = 1; s < 8; ++s) {  // in slice order; zeros past the last
+          acc.x += v[i][s].x;
+          acc.y += v[i][s].y;
+          acc.z += v[i][s].z;
+          acc.w += v[i][s].w;
+        }
+        float y[4] = {fmaf(acc.x * sa[i], sw.x, bf16_lo(bw.x)), fmaf(acc.y * sa[i], sw.y, bf16_hi(bw.x)),
+                      fmaf(acc.z * sa[i], sw.z, bf16_lo(bw.y)), fmaf(acc.w * sa[i], sw.w, bf16_hi(bw.y))};
+        if (p.epi == 1) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[e] = gelu_tanh_f32(y[e]);
+        }
+        *reinterpret_cast<uint2*>(p.Y + static_cast<int64_t>(m) * p.ldy + n) =
+            make_uint2(pack_bf16x2(y[0] + bf16_lo(res[i].x), y[1] + bf16_hi(res[i].x)),
+                       pack_bf16x2(y[2] + bf16_lo(res[i].y), y[3] + bf16_hi(res[i].y)));
+      }
     }
   }
   tc_fence_before();

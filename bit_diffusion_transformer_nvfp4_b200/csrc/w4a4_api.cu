@@ -738,11 +738,44 @@ int launch_fp8_pair(const uint8_t* A8, int64_t lda, const uint8_t* W8, int64_t l
 
 // K slices of the kernel for few rows: a power of two up to a cluster of
 // eight, at most one per 128-deep step, while the CTAs still fit on the device
-// at once (two per SM).
+// at once: two per SM, but clusters of four and eight do not pack that densely
+// (9216 x 3200 at one token: 144 CTAs in pairs 8.2 us, 288 in fours 12.2 us;
+// 6144 x 6144: 192 in fours 11.2 us, 96 in pairs 11.7 us).
 int fp8_small_splits(int64_t n_tiles, int64_t k_steps, int64_t sms) {
   int s = 1;
-  while (s < 8 && 2 * s <= k_steps && n_tiles * 2 * s <= 2 * sms) s *= 2;
+  while (s < 8 && 2 * s <= k_steps && n_tiles * 2 * s <= (s == 1 ? 2 * sms : sms + sms / 2)) s *= 2;
   return s;
+}
+
+// Which FP8 kernel a product takes, by its time on one B200 in units of 10 ns,
+// fitted to products of 1 to 9216 rows, 640 to 18432 columns and K from 512
+// to 8192 (most within 15 %).  Pairs: waves of tiles times K steps times the
+// step (256 x 64, 128 and 256 tiles: 0.20, 0.25, 0.41 us), and a beginning and
+// end.  Few rows: the K steps of a slice, dearer with more tokens a tile and
+// with more than one CTA on an SM, and the exchange of the partial sums.
+// Measured on both sides: 128 x 9216 x 3200 16.4 us by the weight, 12.4 by
+// pairs; 64 x 18432 x 6144 25.4 and 31.0; 333 x 2056 x 4112 13.1, 16.0 and 19.9
+// with tiles 64, 128 and 256 wide, 640 x 6144 x 6144 40.6, 28.3 and 26.0.
+// Returns 0 for the kernel for few rows, else the tile width.
+int fp8_gemm_plan(int64_t M, int64_t N, int64_t K, int64_t sms) {
+  const int64_t k_steps = ceil_div(K, 128), n_tiles = ceil_div(N, 128);
+  int best = 256;
+  int64_t cost = INT64_MAX;
+  const int width[3] = {64, 128, 256}, step[3] = {20, 25, 41}, ends[3] = {350, 450, 700};
+  for (int i = 0; i < 3; ++i) {
+    const int64_t waves = ceil_div(ceil_div(M, 256) * ceil_div(N, width[i]), sms / 2);
+    const int64_t c = waves * k_steps * step[i] + ends[i];
+    if (c < cost) {
+      cost = c;
+      best = width[i];
+    }
+  }
+  if (M <= 128 && n_tiles <= 65535) {
+    const int s = fp8_small_splits(n_tiles, k_steps, sms);
+    const int64_t c = 480 + 340 * M / 128 + ceil_div(k_steps, s) * (26 + 35 * M / 128) * std::max(n_tiles * s, sms) / sms;
+    if (M <= 16 || c < cost) best = 0;
+  }
+  return best;
 }
 
 template <class C>
@@ -1315,16 +1348,16 @@ int fp8_gemm(const uint8_t* A8, int64_t lda, const float* s_a, int s_a_rows, int
   p.epi = epilogue;
   p.status = dev->status_ptr;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (M <= 128 && ceil_div(N, 128) <= 65535) {
-    if (M <= 16) return launch_fp8_small<Fp8Small16>(A8, lda, W8, ldw, p, s, dev);
-    if (M <= 32) return launch_fp8_small<Fp8Small32>(A8, lda, W8, ldw, p, s, dev);
-    if (M <= 64) return launch_fp8_small<Fp8Small64>(A8, lda, W8, ldw, p, s, dev);
-    return launch_fp8_small<Fp8Small128>(A8, lda, W8, ldw, p, s, dev);
+  switch (fp8_gemm_plan(M, N, K, dev->num_sms)) {
+    case 0:
+      if (M <= 16) return launch_fp8_small<Fp8Small16>(A8, lda, W8, ldw, p, s, dev);
+      if (M <= 32) return launch_fp8_small<Fp8Small32>(A8, lda, W8, ldw, p, s, dev);
+      if (M <= 64) return launch_fp8_small<Fp8Small64>(A8, lda, W8, ldw, p, s, dev);
+      return launch_fp8_small<Fp8Small128>(A8, lda, W8, ldw, p, s, dev);
+    case 64: return launch_fp8_pair<Fp8Pair64>(A8, lda, W8, ldw, p, s, dev);
+    case 128: return launch_fp8_pair<Fp8Pair128>(A8, lda, W8, ldw, p, s, dev);
+    default: return launch_fp8_pair<Fp8Pair256>(A8, lda, W8, ldw, p, s, dev);
   }
-  const int64_t pairs = dev->num_sms / 2, m_tiles = ceil_div(M, 256);
-  if (m_tiles * ceil_div(N, 128) <= pairs) return launch_fp8_pair<Fp8Pair64>(A8, lda, W8, ldw, p, s, dev);
-  if (m_tiles * ceil_div(N, 256) <= pairs) return launch_fp8_pair<Fp8Pair128>(A8, lda, W8, ldw, p, s, dev);
-  return launch_fp8_pair<Fp8Pair256>(A8, lda, W8, ldw, p, s, dev);
 }
 
 int cross_attention_bf16(const void* Q, int64_t ldq, const void* K, int64_t ldk, const void* V, int64_t ldv,
