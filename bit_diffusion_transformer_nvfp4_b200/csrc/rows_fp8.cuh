@@ -13,7 +13,7 @@
 // input is read once and every output written once.  That traffic (for
 // x, r, hidden and codes 7 bytes an element) is the bound.
 //
-// Two shapes: rows of up to 1024 columns take a power of two of lanes of one
+// Two shapes: rows of up to 2048 columns take a power of two of lanes of one
 // warp (shuffles only); wider ones a block of their own, a thread holding V
 // 16-byte vectors of the row.
 #pragma once
@@ -22,9 +22,10 @@
 
 namespace w4a4 {
 
-constexpr int kRowsMaxCols = 32768;    // 1024 threads of four vectors of eight
-constexpr int kRowsWarpCols = 1024;    // one warp, four vectors a lane
-constexpr int kRowsWarpThreads = 256;  // block size of the warp-per-row shape
+constexpr int kRowsWarpThreads = 256;   // block size of the warp-per-row shape
+constexpr int kRowsWarpVecs = 8;        // 16-byte vectors a lane holds at most
+constexpr int kRowsBlockThreads = 512;  // most threads of the block-per-row shape
+constexpr int kRowsMaxCols = kRowsBlockThreads * 8 * 8;
 
 struct RowsFp8Params {
   const __nv_bfloat16* x;
@@ -36,55 +37,65 @@ struct RowsFp8Params {
   float* scales;
   int64_t rows, ldx, ldr, ldh, ldn, ldo;
   int cols;
-  float eps;
+  float eps, inv_cols;      // 1 / cols
 };
 
 struct RowStats {
   float sum, top;  // sum of h^2, max |v|
 };
 
-// This thread's vectors t0, t0 + step, ... of the row: loads, hidden, v and
-// the partial statistics.
+// This thread's vectors t0, t0 + step, ... of a row, as loaded.
+template <int V>
+struct RowRaw {
+  uint4 x[V], r[V];
+};
+
 template <int V, bool NORM>
-__device__ __forceinline__ RowStats rows_load(const RowsFp8Params& p, int64_t row, int t0, int step,
-                                              float (&v)[8 * V]) {
+__device__ __forceinline__ void rows_fetch(const RowsFp8Params& p, int64_t row, bool live, int t0, int step,
+                                           RowRaw<V>& raw) {
   const int nv = p.cols >> 3;
-  uint4 xw[V], rw[V];
   const uint4* xr = reinterpret_cast<const uint4*>(p.x + row * p.ldx);
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int t = t0 + i * step;
-    xw[i] = t < nv ? xr[t] : make_uint4(0u, 0u, 0u, 0u);
+    raw.x[i] = live && t < nv ? xr[t] : make_uint4(0u, 0u, 0u, 0u);
   }
   if (NORM && p.r != nullptr) {
     const uint4* rr = reinterpret_cast<const uint4*>(p.r + row * p.ldr);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int t = t0 + i * step;
-      rw[i] = t < nv ? rr[t] : make_uint4(0u, 0u, 0u, 0u);
+      raw.r[i] = live && t < nv ? rr[t] : make_uint4(0u, 0u, 0u, 0u);
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) rw[i] = make_uint4(0u, 0u, 0u, 0u);
   }
+}
+
+// hidden, v and the partial statistics.
+template <int V, bool NORM>
+__device__ __forceinline__ RowStats rows_take(const RowsFp8Params& p, int64_t row, bool live, int t0, int step,
+                                              const RowRaw<V>& raw, float (&v)[8 * V]) {
+  const int nv = p.cols >> 3;
   RowStats st = {0.0f, 0.0f};
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const uint32_t xs[4] = {xw[i].x, xw[i].y, xw[i].z, xw[i].w};
-    const uint32_t rs[4] = {rw[i].x, rw[i].y, rw[i].z, rw[i].w};
+    const uint32_t xs[4] = {raw.x[i].x, raw.x[i].y, raw.x[i].z, raw.x[i].w};
     float* vi = v + 8 * i;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       vi[2 * j] = bf16_lo(xs[j]);
       vi[2 * j + 1] = bf16_hi(xs[j]);
-      if (NORM && p.r != nullptr) {
-        vi[2 * j] += bf16_lo(rs[j]);
-        vi[2 * j + 1] += bf16_hi(rs[j]);
-      }
     }
     const int t = t0 + i * step;
     if (NORM) {
-      if (p.hidden != nullptr && t < nv)
+      if (p.r != nullptr) {
+        const uint32_t rs[4] = {raw.r[i].x, raw.r[i].y, raw.r[i].z, raw.r[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          vi[2 * j] += bf16_lo(rs[j]);
+          vi[2 * j + 1] += bf16_hi(rs[j]);
+        }
+      }
+      if (p.hidden != nullptr && live && t < nv)
         reinterpret_cast<uint4*>(p.hidden + row * p.ldh)[t] =
             make_uint4(pack_bf16x2(vi[0], vi[1]), pack_bf16x2(vi[2], vi[3]), pack_bf16x2(vi[4], vi[5]),
                        pack_bf16x2(vi[6], vi[7]));
@@ -111,12 +122,17 @@ template <int V, bool NORM>
 __device__ __forceinline__ void rows_store(const RowsFp8Params& p, int64_t row, int t0, int step, bool first,
                                            RowStats st, const float (&v)[8 * V]) {
   const int nv = p.cols >> 3;
-  const float inv = NORM ? 1.0f / sqrtf(st.sum / static_cast<float>(p.cols) + p.eps) : 1.0f;
+  // the norm's factor and quotients by the hardware's reciprocals (a few
+  // units of the 23rd bit; the plain codes' are exact divisions, whose steps
+  // their definition fixes): every lane of a short row does these
+  const float inv = NORM ? rsqrtf(fmaf(st.sum, p.inv_cols, p.eps)) : 1.0f;
   if (p.codes != nullptr) {
-    float s = (NORM ? st.top * inv : st.top) / 448.0f;
-    if (!(s >= 1.17549435e-38f && s < INFINITY)) s = 1.0f;
+    float s = NORM ? st.top * inv * (1.0f / 448.0f) : st.top / 448.0f;
+    const bool normal = s >= 1.17549435e-38f && s < INFINITY;
+    if (!normal) s = 1.0f;
     if (first) p.scales[row] = s;
-    const float f = NORM ? inv * (1.0f / s) : 1.0f / s;
+    // (i / s = 448 / max|v|)
+    const float f = !normal ? inv : NORM ? __fdividef(448.0f, st.top) : 1.0f / s;
     uint2* out = reinterpret_cast<uint2*>(p.codes + row * p.ldo);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -140,18 +156,21 @@ __device__ __forceinline__ void rows_store(const RowsFp8Params& p, int64_t row, 
   }
 }
 
-// A row per `lanes` lanes (a power of two up to 32) of a warp.
+// A row per `lanes` lanes (a power of two up to 32) of a warp: no barriers, and
+// as many vectors a lane as there are up to kRowsWarpVecs, so that the
+// reduction and the row's quotients are shared by many elements (a 128-column
+// row on 16 lanes of one vector took 7.2 us for 36888 rows).
 template <int V, bool NORM>
 __global__ void __launch_bounds__(kRowsWarpThreads) rows_fp8_warp_kernel(const RowsFp8Params p, int lanes) {
   grid_launch_dependents();
   grid_dependency_wait();
-  const int per_block = kRowsWarpThreads / lanes;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * per_block + threadIdx.x / lanes;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kRowsWarpThreads / lanes) + threadIdx.x / lanes;
   const int t0 = threadIdx.x & (lanes - 1);
-  const bool live = row < p.rows;  // the shuffles below take whole warps
+  const bool live = row < p.rows;  // (the shuffles take whole warps)
+  RowRaw<V> raw;
+  rows_fetch<V, NORM>(p, row, live, t0, lanes, raw);
   float v[8 * V];
-  RowStats st = {0.0f, 0.0f};
-  if (live) st = rows_load<V, NORM>(p, row, t0, lanes, v);
+  RowStats st = rows_take<V, NORM>(p, row, live, t0, lanes, raw, v);
   for (int o = lanes >> 1; o > 0; o >>= 1) {
     if (NORM) st.sum += __shfl_xor_sync(0xffffffffu, st.sum, o);
     st.top = fmaxf(st.top, __shfl_xor_sync(0xffffffffu, st.top, o));
@@ -161,14 +180,16 @@ __global__ void __launch_bounds__(kRowsWarpThreads) rows_fp8_warp_kernel(const R
 
 // A row per block.
 template <int V, bool NORM>
-__global__ void __launch_bounds__(1024) rows_fp8_block_kernel(const RowsFp8Params p) {
+__global__ void __launch_bounds__(kRowsBlockThreads) rows_fp8_block_kernel(const RowsFp8Params p) {
   __shared__ float red_sum[32], red_top[32];
   grid_launch_dependents();
   grid_dependency_wait();
   const int64_t row = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  RowRaw<V> raw;
+  rows_fetch<V, NORM>(p, row, true, threadIdx.x, blockDim.x, raw);
   float v[8 * V];
-  RowStats st = rows_load<V, NORM>(p, row, threadIdx.x, blockDim.x, v);
+  RowStats st = rows_take<V, NORM>(p, row, true, threadIdx.x, blockDim.x, raw, v);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     if (NORM) st.sum += __shfl_xor_sync(0xffffffffu, st.sum, o);

@@ -37,6 +37,7 @@ struct DeviceInfo {
   bool ok = false;
   int num_sms = 0;
   int* status_ptr = nullptr;
+  int xattn_clusters[9] = {};  // clusters of 1 .. 8 of the split cross attention that are resident at once
 };
 DeviceInfo g_dev[kMaxDevices];
 std::mutex g_mu;
@@ -146,6 +147,24 @@ int device_setup(DeviceInfo** out) {
              smem_attr<XAttnCfg<2, false>>(cross_attention_kernel<XAttnCfg<2, false>>) &&
              smem_attr<XAttnCfg<1, true>>(cross_attention_kernel<XAttnCfg<1, true>>) &&
              smem_attr<XAttnCfg<2, true>>(cross_attention_kernel<XAttnCfg<2, true>>);
+
+  // (one CTA per SM; clusters stay within a GPC, so larger ones leave SMs over)
+  for (int c = 1; c <= 8; ++c) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(c), static_cast<unsigned>(d.num_sms), 1);
+    cfg.blockDim = dim3(kXThreads, 1, 1);
+    cfg.dynamicSmemBytes = XAttnCfg<2, true>::SMEM;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(c);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    attr_ok &= cudaOccupancyMaxActiveClusters(&n, cross_attention_kernel<XAttnCfg<2, true>>, &cfg) == cudaSuccess;
+    d.xattn_clusters[c] = std::max(n, 1);
+  }
 
   if (!attr_ok) { cudaGetLastError(); return W4A4_ERR_CUDA; }
   d.ok = true;
@@ -672,22 +691,31 @@ int launch_rows_fp8(const RowsFp8Params& p, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cudaError_t e;
-  if (p.cols <= kRowsWarpCols) {
+  if (nv <= (NORM ? 128 : 32 * kRowsWarpVecs)) {
+    // a row per group of lanes: four vectors a lane while that fills no warp.
+    // (Up to 2048 columns for the codes alone, 9000 x 1032: 5.7 us against 9.9
+    // with a block a row; the norm keeps the residual too and gains only up
+    // to 1024 columns, 9000 x 2048: 29.9 us against 22.7.)
     int lanes = 1;
-    while (lanes < 32 && lanes < nv) lanes *= 2;
-    const int64_t per_block = kRowsWarpThreads / lanes;
-    cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(p.rows, per_block)), 1, 1);
+    while (lanes < 32 && 4 * lanes < nv) lanes *= 2;
+    cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(p.rows, kRowsWarpThreads / lanes)), 1, 1);
     cfg.blockDim = dim3(kRowsWarpThreads, 1, 1);
-    e = nv <= 32   ? cudaLaunchKernelEx(&cfg, rows_fp8_warp_kernel<1, NORM>, p, lanes)
-        : nv <= 64 ? cudaLaunchKernelEx(&cfg, rows_fp8_warp_kernel<2, NORM>, p, lanes)
-                   : cudaLaunchKernelEx(&cfg, rows_fp8_warp_kernel<4, NORM>, p, lanes);
+    if constexpr (NORM) {
+      e = cudaLaunchKernelEx(&cfg, rows_fp8_warp_kernel<4, true>, p, lanes);
+    } else {
+      e = nv <= 128   ? cudaLaunchKernelEx(&cfg, rows_fp8_warp_kernel<4, false>, p, lanes)
+          : nv <= 192 ? cudaLaunchKernelEx(&cfg, rows_fp8_warp_kernel<6, false>, p, lanes)
+                      : cudaLaunchKernelEx(&cfg, rows_fp8_warp_kernel<kRowsWarpVecs, false>, p, lanes);
+    }
   } else {
-    const int vecs = nv <= 512 ? 1 : nv <= 2048 ? 2 : 4;
+    // a row per block of up to 512 threads: four vectors a thread, eight for
+    // wide rows (codes of 2000 x 16384: 16.6 us with eight, 18.1 with four;
+    // norm of 1000 x 16384: 29.2 us with eight, 23.4 with four)
+    const int vecs = nv <= (NORM ? 2048 : 1024) ? 4 : 8;
     cfg.gridDim = dim3(static_cast<unsigned>(p.rows), 1, 1);
     cfg.blockDim = dim3(static_cast<unsigned>(ceil_div(ceil_div(nv, vecs), 32) * 32), 1, 1);
-    e = vecs == 1   ? cudaLaunchKernelEx(&cfg, rows_fp8_block_kernel<1, NORM>, p)
-        : vecs == 2 ? cudaLaunchKernelEx(&cfg, rows_fp8_block_kernel<2, NORM>, p)
-                    : cudaLaunchKernelEx(&cfg, rows_fp8_block_kernel<4, NORM>, p);
+    e = vecs == 4 ? cudaLaunchKernelEx(&cfg, rows_fp8_block_kernel<4, NORM>, p)
+                  : cudaLaunchKernelEx(&cfg, rows_fp8_block_kernel<8, NORM>, p);
   }
   if (e != cudaSuccess) {
     cudaGetLastError();
@@ -827,25 +855,24 @@ bool encode_heads(CUtensorMap* m, const void* ptr, int64_t D, int64_t heads, int
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Which form a problem takes: splits == 0 the persistent one (256 rows a work
-// tile), else the split one (128 rows) with that many CTAs of a cluster on the
-// keys of a tile.  Both are costed in key tiles run one after another.
-struct XPlan {
-  int splits = 0;
-};
-
-XPlan xattn_plan(int64_t rows, int64_t head_blocks, int64_t key_tiles, int64_t sms) {
-  XPlan best;
-  // persistent: two row tiles against a key tile at a time, about 2.2 units
-  // (a unit: one softmax stream's tile in the split form), 2 to begin and end
-  int64_t cost = ceil_div(ceil_div(rows, 2 * kXTile) * head_blocks, sms) * (22 * key_tiles + 20);
+// Which form a problem takes: 0 the persistent one (256 rows a work tile), else
+// the split one (128 rows) with that many CTAs of a cluster on the keys of a
+// tile, by their time on one B200 in units of 0.1 us.  Persistent: 1.7 us a
+// key tile and 3 us a work tile, one after the other on an SM.  Split: 7 us
+// and 1.4 us a key tile, in waves of the clusters that are resident at once
+// (B200: 74 of two, 33 of four, 15 of eight).
+// Measured: 4 x 1 query, 4109 keys, 32 heads on 8: 18.8 us in fours; 1 query,
+// 4096 keys, 16 heads: 21.5 us in eights (two waves of clusters).
+int xattn_splits(int64_t rows, int64_t head_blocks, int64_t key_tiles, const DeviceInfo& dev) {
+  int best = 0;
+  int64_t cost = ceil_div(ceil_div(rows, 2 * kXTile) * head_blocks, dev.num_sms) * (17 * key_tiles + 30) + 30;
   const int64_t units = ceil_div(rows, kXTile) * head_blocks;
   if (units > 65535) return best;
-  for (int s = 1; s <= 8 && s <= key_tiles; s *= 2) {
-    const int64_t c = ceil_div(units * s, sms) * (12 * ceil_div(key_tiles, s) + 25 + 5 * (s > 1));
+  for (int s = 1; s <= 8 && s <= key_tiles; ++s) {
+    const int64_t c = ceil_div(units, dev.xattn_clusters[s]) * (14 * ceil_div(key_tiles, s) + 70);
     if (c < cost) {
       cost = c;
-      best.splits = s;
+      best = s;
     }
   }
   return best;
@@ -1311,6 +1338,7 @@ int rmsnorm_fp8(const void* X, int64_t rows, int64_t cols, int64_t ldx, const vo
   p.ldn = ldn;
   p.ldo = ldo;
   p.eps = eps;
+  p.inv_cols = 1.0f / static_cast<float>(cols);
   return launch_rows_fp8<true>(p, static_cast<cudaStream_t>(stream));
 }
 
@@ -1412,11 +1440,10 @@ int cross_attention_bf16(const void* Q, int64_t ldq, const void* K, int64_t ldk,
   p.O = static_cast<__nv_bfloat16*>(O);
   p.ldo = ldo;
   p.status = dev->status_ptr;
-  const XPlan plan = xattn_plan(Sq * p.pack, batch * (heads / p.pack), ceil_div(Skv, kXTile), dev->num_sms);
-  if (plan.splits > 0)
-    return d_head <= 64
-               ? launch_cross_attention<XAttnCfg<1, true>>(Q, ldq, K, ldk, V, ldv, p, plan.splits, s, dev)
-               : launch_cross_attention<XAttnCfg<2, true>>(Q, ldq, K, ldk, V, ldv, p, plan.splits, s, dev);
+  const int splits = xattn_splits(Sq * p.pack, batch * (heads / p.pack), ceil_div(Skv, kXTile), *dev);
+  if (splits > 0)
+    return d_head <= 64 ? launch_cross_attention<XAttnCfg<1, true>>(Q, ldq, K, ldk, V, ldv, p, splits, s, dev)
+                        : launch_cross_attention<XAttnCfg<2, true>>(Q, ldq, K, ldk, V, ldv, p, splits, s, dev);
   return d_head <= 64 ? launch_cross_attention<XAttnCfg<1, false>>(Q, ldq, K, ldk, V, ldv, p, 1, s, dev)
                       : launch_cross_attention<XAttnCfg<2, false>>(Q, ldq, K, ldk, V, ldv, p, 1, s, dev);
 }
