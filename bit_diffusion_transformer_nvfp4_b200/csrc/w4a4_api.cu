@@ -162,8 +162,11 @@ int device_setup(DeviceInfo** out) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int n = 0;
-    attr_ok &= cudaOccupancyMaxActiveClusters(&n, cross_attention_kernel<XAttnCfg<2, true>>, &cfg) == cudaSuccess;
-    d.xattn_clusters[c] = std::max(n, 1);
+    if (cudaOccupancyMaxActiveClusters(&n, cross_attention_kernel<XAttnCfg<2, true>>, &cfg) != cudaSuccess || n < 1) {
+      cudaGetLastError();
+      n = std::max(d.num_sms / c, 1);  // (only a cost: the launch is valid either way)
+    }
+    d.xattn_clusters[c] = n;
   }
 
   if (!attr_ok) { cudaGetLastError(); return W4A4_ERR_CUDA; }
@@ -1405,7 +1408,7 @@ int cross_attention_bf16(const void* Q, int64_t ldq, const void* K, int64_t ldk,
   if (Sq * ldq >= bytes_max || Skv * ldk >= bytes_max || Skv * ldv >= bytes_max || Sq * ldo >= bytes_max ||
       batch * heads * ceil_div(Sq, 4) > (int64_t(1) << 30))
     return W4A4_ERR_SHAPE;
-  if (!(softmax_scale > 0.0f) || !(softmax_scale < 3.0e38f)) return W4A4_ERR_ARG;
+  if (!(softmax_scale > 0.0f) || !(softmax_scale < 2.3e38f)) return W4A4_ERR_ARG;  // (times log2 e it stays finite)
   if (batch == 0 || Sq == 0) return W4A4_OK;
   if (!O || (Skv > 0 && (!Q || !K || !V))) return W4A4_ERR_NULL;
   if (!aligned16(Q) || !aligned16(K) || !aligned16(V) || !aligned16(O) || reinterpret_cast<uintptr_t>(kv_len) % 4 != 0)

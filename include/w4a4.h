@@ -440,7 +440,7 @@ int fp8_quantize_rows(const void* X, int64_t rows, int64_t cols, int64_t ldx, ui
  *                 nvfp4_quantize_act, for a W4A4 layer after the norm)
  *   codes, scales  out as in fp8_quantize_rows; codes NULL: neither is
  *                 written (then normed must be given)
- * Sizes and strides as in fp8_quantize_rows.
+ * Sizes and strides as in fp8_quantize_rows.  A zero row with eps 0 is NaN.
  */
 int rmsnorm_fp8(const void* X, int64_t rows, int64_t cols, int64_t ldx, const void* R, int64_t ldr,
                 const void* weight, float eps, void* hidden, int64_t ldh, void* normed, int64_t ldn,
@@ -479,14 +479,15 @@ int fp8_gemm(const uint8_t* A8, int64_t lda, const float* s_a, int s_a_rows, int
  *             keys count (values outside 0 .. Skv are taken as the nearest)
  *   key_mask  in  uint8 device [kv_batch, ld_mask] or NULL: keys with 0 do
  *             not count
- *   softmax_scale  c (normally 1/sqrt(d_head)), finite and > 0
+ *   softmax_scale  c (normally 1/sqrt(d_head)), > 0 and < 2.3e38
  *   O     out bf16 [batch * Sq, ldo]
  * Keys that do not count may hold anything, NaN included.  A query without a
  * key gets 0.  A counted score that is NaN or +infinity makes its row NaN.
  * fp32 scores, sums and accumulation; the probabilities are rounded to bf16
  * for the second product.  Strides are in elements, multiples of 8 (ld_mask:
- * any, >= Skv); Sq, Skv <= 2^24.  No workspace; results do not depend on
- * timing.
+ * any, >= Skv); Sq, Skv <= 2^24, batch and heads <= 65535, batch * heads *
+ * ceil(Sq / 4) <= 2^30, a sequence's rows below 2^39 elements.  No workspace;
+ * results do not depend on timing.
  */
 int cross_attention_bf16(const void* Q, int64_t ldq, const void* K, int64_t ldk, const void* V, int64_t ldv,
                          int64_t batch, int64_t kv_batch, int64_t Sq, int64_t Skv, int64_t heads, int64_t kv_heads,

@@ -119,7 +119,8 @@ def test_cross_attention_arguments(so):
     assert call(Skv=(1 << 24) + 1) == -2
     assert call(Sq=1 << 24, ldq=1 << 20) == -2     # the batch stride leaves its field
     assert call(mask=P, ldm=19) == -2
-    for c in (0.0, -1.0, float("nan"), float("inf")):
+    assert call(batch=40000, kv_batch=1, heads=40000, kv_heads=1, d=8, Sq=1, ldq=320000, ldo=320000) == -2  # tile count
+    for c in (0.0, -1.0, float("nan"), float("inf"), 2.5e38):
         assert call(c=c) == -8
     for name in ("Q", "K", "V", "O"):
         assert call(**{name: None}) == -1, name

@@ -229,6 +229,23 @@ def test_linear_exact_sums(w4, M, N, K, gelu, bias, residual):
     assert np.all(err <= bound), (np.max(err / bound), np.unravel_index(np.argmax(err / bound), err.shape))
 
 
+@pytest.mark.parametrize("M,N,K", [(1100, 2312, 4112), (1000, 9400, 2064), (2000, 9400, 2064)])
+def test_linear_wide_tiles(w4, M, N, K):
+    """256-column tiles: one, two and four a CTA pair, ragged on both sides."""
+    g = rng(M + N)
+    a, s_a, w, s_w, b, r = integer_case(g, M, N, K, True, True)
+    A = w4.Fp8Rows(dev_u8(a), to_dev_f32(s_a))
+    W = w4.PackedWeightFp8(dev_u8(w), to_dev_f32(s_w), to_dev_bf16(b))
+    Y = w4.linear_fp8(A, W, activation=w4.EPI_GELU_TANH, residual=to_dev_bf16(r))
+    # codes of whole and half units: fp32 products of 2 a and 2 w are exact below 2^24
+    acc = (2 * oblock.decode(a)).astype(np.float32) @ (2 * oblock.decode(w)).astype(np.float32).T
+    t = acc.astype(np.float64) / 4 * s_a[:, None].astype(np.float64) * s_w[None, :]
+    want = oblock.gelu_tanh(t + b) + r
+    bound = BF16 * np.abs(want) + 2.0 ** -19 * (np.abs(t) + np.abs(b) + np.abs(r)) + 2.0 ** -133
+    err = np.abs(from_dev_bf16(Y) - want)
+    assert np.all(err <= bound), np.max(err / bound)
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 768, 3328), (48, 520, 2048), (500, 776, 4096), (1500, 2048, 1552)])
 def test_linear_random_codes(w4, M, N, K):
     g = rng(M + N + K)
