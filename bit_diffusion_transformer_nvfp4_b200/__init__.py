@@ -484,24 +484,35 @@ def _vector(name, t, dtype, dev, n):
 def _launch(fn, dev, stream, *args):
     """Calls an entry point with ``dev`` current (the library works on the
     current device) on the given stream or ``dev``'s current one."""
-    current = torch.cuda.current_device()
     if stream is None:
         stream = torch._C._cuda_getCurrentRawStream(dev)
     else:
         stream = getattr(stream, "cuda_stream", stream)
-    if current == dev:
-        _check(fn, getattr(lib(), fn)(*args, stream))
-        return
-    with torch.cuda.device(dev):
-        _check(fn, getattr(lib(), fn)(*args, stream))
+    call = getattr(_lib or lib(), fn)
+    if torch._C._cuda_getDevice() == dev:
+        status = call(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            status = call(*args, stream)
+    if status != 0:
+        raise W4A4Error(fn, status)
 
 
 class Fp8Rows:
     """E4M3 codes (uint8 [rows, cols]) with one fp32 scale per row."""
 
+    __slots__ = ("codes", "scales")
+
     def __init__(self, codes, scales):
         self.codes, self.scales = codes, scales
-        self.rows, self.cols = codes.shape
+
+    @property
+    def rows(self):
+        return self.codes.shape[0]
+
+    @property
+    def cols(self):
+        return self.codes.shape[1]
 
 
 class PackedWeightFp8:
@@ -516,7 +527,7 @@ class PackedWeightFp8:
 def _row_outputs(rows, cols, dev, device, codes, scales):
     """(codes, their row stride, scales), made where they are None."""
     if codes is None:
-        codes, ldo = torch.empty((rows, cols), dtype=torch.uint8, device=device), cols
+        codes, ldo = torch.empty(rows, cols, dtype=torch.uint8, device=device), cols
     else:
         ldo = _matrix("codes", codes, torch.uint8, dev, rows, cols)
     if scales is None:
@@ -556,7 +567,7 @@ def rms_norm_fp8(X, weight=None, residual=None, eps=1e-6, hidden=None, normed=No
     if hidden is not None:
         ldh = _matrix("hidden", hidden, torch.bfloat16, dev, rows, cols)
     elif residual is not None:
-        hidden, ldh = torch.empty((rows, cols), dtype=torch.bfloat16, device=X.device), cols
+        hidden, ldh = torch.empty(rows, cols, dtype=torch.bfloat16, device=X.device), cols
     if hidden is not None:
         h = hidden.data_ptr()
     if normed is not None:
@@ -600,7 +611,7 @@ def linear_fp8(a, w: PackedWeightFp8, activation: int = EPI_NONE, residual=None,
         ldr = _matrix("residual", residual, torch.bfloat16, dev, M, N)
         r = residual.data_ptr()
     if Y is None:
-        Y, ldy = torch.empty((M, N), dtype=torch.bfloat16, device=codes.device), N
+        Y, ldy = torch.empty(M, N, dtype=torch.bfloat16, device=codes.device), N
     else:
         ldy = _matrix("Y", Y, torch.bfloat16, dev, M, N)
     _launch("fp8_gemm", dev, stream, codes.data_ptr(), lda, s_a.data_ptr(), int(per_row), M, N, K, w.codes.data_ptr(),
@@ -641,7 +652,7 @@ def cross_attention(q, k, v, heads: int, kv_heads=None, batch: int = 1, kv_batch
                                kv_batch, Skv))
         m = key_mask.data_ptr()
     if O is None:
-        O, ldo = torch.empty((rows, width), dtype=torch.bfloat16, device=q.device), width
+        O, ldo = torch.empty(rows, width, dtype=torch.bfloat16, device=q.device), width
     else:
         ldo = _matrix("O", O, torch.bfloat16, dev, rows, width)
     c = 1.0 / math.sqrt(d) if softmax_scale is None else softmax_scale
