@@ -32,7 +32,7 @@
 #pragma once
 
 #include "attention.cuh"
-#include "sm100.cuh"
+#include "sm100_warp.cuh"
 
 namespace w4a4 {
 
@@ -42,7 +42,7 @@ constexpr int kXThreads = 512;    // control warpgroup, a softmax warpgroup a st
 constexpr float kXSlack = 8.0f;   // binades a tile's maximum may pass the offset
 constexpr int kXChunk = 16;       // scores taken together through the exponential
 constexpr int kXPolyPairs = 2;    // of 16 pairs of exponentials, how many on the FMA pipes instead of the MUFU
-constexpr int kXRegsCtrl = 80, kXRegsSoftmax = 160, kXRegsEpi = 112;  // of 128 at launch
+constexpr int kXRegsCtrl = 80, kXRegsSoftmax = 168, kXRegsEpi = 96;  // of 128 at launch
 static_assert(128 * (kXRegsCtrl + kXRegsEpi) + 256 * kXRegsSoftmax <= kXThreads * 128,
               "register budgets fit the launch allocation");
 
@@ -668,7 +668,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
     const int q = warp & 3;  // TMEM lane quarter
     const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
     uint8_t* boxes = smem + C::O_OFF + q * (2 * 32 * 128);
-    uint32_t closed = 0, stores = 0;  // tiles with keys done; boxes filled
+    uint32_t closed = 0;  // tiles with keys done
     bool ok = !SPLIT;
     for (XWalk w(p, first); w.live(p) && ok; w.next(p)) {
       const XTileAt a = w.at(p, kRows);
@@ -684,47 +684,48 @@ __global__ void __launch_bounds__(kXThreads, 1)
           tc_fence_after();
           f = reinterpret_cast<const float*>(smem + C::F_OFF)[t * kXTile + q * 32 + lane];
         }
-        // the row's sums out of TMEM at once, so that the next tile's first
-        // product can overwrite them
-        uint32_t b[DB * 32];
+        // out of TMEM and into the boxes as fast as it goes: the next tile's
+        // first product waits to overwrite the sums
+        if (lane == 0) bulk_wait_group_read<0>();  // the boxes' last stores have been read
+        __syncwarp();
 #pragma unroll
         for (int hh = 0; hh < DB * 2; ++hh) {
           uint32_t v[32];
           if (some) {
             tmem_ld_32cols(tmem + C::O_COL + 128 * t + lane_base + 32 * hh, v);
             tmem_ld_wait();
+            if (hh == DB * 2 - 1) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(smem_u32(&o_free[t]));
+            }
           } else {
 #pragma unroll
             for (int e = 0; e < 32; ++e) v[e] = 0u;
           }
+          uint8_t* row = boxes + (hh >> 1) * (32 * 128) + lane * 128;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float o0, o1;
-            mul2_rn(o0, o1, __uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]), f, f);
-            b[16 * hh + e] = pack_bf16x2(o0, o1);
+          for (int u = 0; u < 4; ++u) {
+            uint32_t b[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float o0, o1;
+              mul2_rn(o0, o1, __uint_as_float(v[8 * u + 2 * e]), __uint_as_float(v[8 * u + 2 * e + 1]), f, f);
+              b[e] = pack_bf16x2(o0, o1);
+            }
+            *reinterpret_cast<uint4*>(row + (((4 * (hh & 1) + u) ^ (lane & 7)) << 4)) =
+                make_uint4(b[0], b[1], b[2], b[3]);
           }
         }
-        if (some) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&o_free[t]));
-        }
+        fence_proxy_async_smem();
+        __syncwarp();
         const int tok0 = (a.row0 + t * kXTile + q * 32) / p.pack;
+        if (lane == 0) {
+          if (tok0 < p.Sq)
 #pragma unroll
-        for (int d = 0; d < DB; ++d, ++stores) {
-          uint8_t* box = boxes + (stores & 1) * (32 * 128);
-          if (lane == 0) bulk_wait_group_read<1>();  // the store before the last has read this box
-          __syncwarp();
-#pragma unroll
-          for (int u = 0; u < 8; ++u)
-            *reinterpret_cast<uint4*>(box + lane * 128 + ((u ^ (lane & 7)) << 4)) =
-                make_uint4(b[32 * d + 4 * u], b[32 * d + 4 * u + 1], b[32 * d + 4 * u + 2], b[32 * d + 4 * u + 3]);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            if (tok0 < p.Sq) tma_store_4d(&tm_o, smem_u32(box), 64 * d, a.h0, tok0, a.b);
-            bulk_commit_group();
-          }
+            for (int d = 0; d < DB; ++d)
+              tma_store_4d(&tm_o, smem_u32(boxes + d * (32 * 128)), 64 * d, a.h0, tok0, a.b);
+          bulk_commit_group();
         }
       }
       if (some) ++closed;

@@ -17,7 +17,7 @@
 
 #include "attention.cuh"
 #include "gemm.cuh"
-#include "sm100.cuh"
+#include "sm100_warp.cuh"
 
 namespace w4a4 {
 
