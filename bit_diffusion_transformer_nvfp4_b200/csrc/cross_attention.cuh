@@ -4,31 +4,48 @@
 // Per query row and head, over the keys j that the length and the key mask
 // leave:  o = sum_j 2^(c q.k_j - m) v_j / sum_j 2^(c q.k_j - m),
 // c = scale log2 e, the sums and the running offset m in fp32; a row without
-// keys gives 0.  m moves only when a tile's maximum passes it by more than
-// kXSlack binades (the accumulator and the sum are then rescaled), which is
-// exact: numerator and denominator share the offset.  The probabilities are
-// rounded to bf16 for the second product, a relative 2^-9 each, random in
-// sign, against the 2^-9 of the output's own rounding.
+// keys gives 0.  m moves only when a half tile's maximum passes it by more
+// than kXSlack binades (the accumulator and the sum are then rescaled), which
+// is exact: numerator and denominator share the offset.  The probabilities
+// are rounded to bf16 for the second product, at most 2^-8 each, random in
+// sign, against the same bound of the output's own rounding.
 //
 // A work tile is 128 rows of one key/value head: queries times the heads that
 // share it (the largest power of two of them, so that a group of heads reads
 // its keys once), loaded by one 4-D TMA box whose row order is token-major.
 // S = Q K^T and O += P V are tcgen05.mma kind::f16 with both accumulators in
 // TMEM; P goes back into S's columns as the A operand of the second product,
-// V is its MN-major B operand as it lies in memory.  MMAs of the issuing
-// thread run in order, so S of the next key tile may follow the product that
-// reads P, and a commit that covers S covers the product before it too; each
-// stream has an issuing warp of its own (issuing takes 45 to 58 cycles an
-// MMA and a wait about 100, so one warp for both left the tensor pipe idle).
+// V is its MN-major B operand as it lies in memory.
 //
-// Two forms, each with two streams of softmax (a warpgroup each, one row a
-// thread) that alternate on the tensor cores:
+// A stream of softmax (a warpgroup, one row a thread) takes a 128-key tile in
+// two halves of 64 with a score buffer each: when a half's probabilities are
+// there its product goes out, and behind it the next tile's scores for the
+// same buffer, so that scores are always ahead.  The issuing thread's MMAs run
+// in order: the scores may follow the product that reads the buffer, and one
+// commit covers both.  Measured on 16384 queries, 4096 keys, 16 heads of 128:
+// one buffer of 128 keys a stream 440 us (the softmax, 1800 cycles a tile, and
+// the MMAs, 1600 with their latency, in turn), this 427 us although the
+// narrower scores cost the pipe more (128 x 64 x 16: 48 cycles from shared
+// memory where 128 x 128 x 16 takes 64); two threads a row, with one buffer,
+// 449 us (a barrier between their halves).
+//
+// Roles (512 threads): a warp each for loading keys and values, loading
+// queries (a query tile waits for the scores of the tile before and would hold
+// up the keys behind it) and issuing each stream's MMAs; two softmax
+// warpgroups; an epilogue warpgroup that normalises and stores a finished tile
+// under the next one.
+//
+// Two forms:
 //   SPLIT = false  many rows: the streams are two row tiles over the same keys,
-//                  persistent CTAs, one per SM; the next tile's first scores
-//                  are computed under this tile's epilogue.
+//                  persistent CTAs, one per SM.  Bound by the tensor pipe (76 %
+//                  busy) and the exponentials (MUFU 54 %), at full load by the
+//                  power cap: 1290 TFLOP/s back to back, 1100 sustained,
+//                  against 1646 and 1388 measured for a large matrix product.
 //   SPLIT = true   few rows: the streams are the even and odd key tiles of one
 //                  row tile, and a cluster of CTAs splits the keys; the
-//                  partial sums meet in (distributed) shared memory.
+//                  partial sums meet in (distributed) shared memory.  Bound by
+//                  the key and value bytes and about 7 us of latency (4 x 1
+//                  query, 4109 keys, 32 heads on 8: 18.2 us, 3.7 TB/s).
 #pragma once
 
 #include "attention.cuh"
@@ -41,7 +58,9 @@ constexpr int kXSub = 64;         // keys of a score buffer
 constexpr int kXThreads = 512;    // control warpgroup, a softmax warpgroup a stream, epilogue warpgroup
 constexpr float kXSlack = 8.0f;   // binades a tile's maximum may pass the offset
 constexpr int kXChunk = 16;       // scores taken together through the exponential
-constexpr int kXPolyPairs = 2;    // of 16 pairs of exponentials, how many on the FMA pipes instead of the MUFU
+// Of 16 pairs of exponentials, how many on the FMA pipes instead of the MUFU
+// (0, 2, 4 and 6: 443, 427, 425 and 428 us on the long case; fewer take less power).
+constexpr int kXPolyPairs = 2;
 constexpr int kXRegsCtrl = 80, kXRegsSoftmax = 168, kXRegsEpi = 96;  // of 128 at launch
 static_assert(128 * (kXRegsCtrl + kXRegsEpi) + 256 * kXRegsSoftmax <= kXThreads * 128,
               "register budgets fit the launch allocation");
@@ -122,8 +141,8 @@ struct XTileAt {
 
 // A role's walk over a CTA's work tiles, gridDim.x apart in the persistent
 // form.  Only the first is decoded by division; each tile's key length is
-// loaded a tile ahead (decoding a tile afresh and loading its length took 3500
-// cycles of every softmax warp, as long as two and a half key halves).
+// loaded a tile ahead (with five divisions and the load in every tile a
+// batch of short prompts took 86.7 us, this way 84.5).
 struct XWalk {
   int tile, rt, hb, b;  // work tile: row tile, head block, sequence
   int len, len1;        // its key length as loaded, and that of the tile behind

