@@ -26,6 +26,7 @@ namespace w4a4 {
 
 struct Fp8GemmParams {
   int M, N, K;
+  int m_group;               // row tiles swept together over all columns (pair kernel)
   const float* s_a;
   int s_a_step;              // 1: one scale per row of A, 0: one for all
   const float* s_w;
@@ -74,6 +75,16 @@ struct Fp8PairCfg {
   static_assert(TMEM_COLS <= 512 && (TMEM_COLS & (TMEM_COLS - 1)) == 0, "TMEM budget");
   static_assert(HALF % 32 == 0 && STAGE_BYTES % 1024 == 0, "tile shape");
 };
+
+// Tile `tile` of a product in row and column tiles: groups of `group` row
+// tiles, each swept over all columns with the row tiles fastest, so that a
+// group's rows of A stay in L2 while W streams past them.
+__device__ __forceinline__ void fp8_tile_at(int tile, int m_tiles, int n_tiles, int group, int& m, int& n) {
+  const int g = tile / (group * n_tiles), r = tile - g * group * n_tiles;
+  const int rows = min(group, m_tiles - g * group);
+  n = r / rows;
+  m = g * group + r - n * rows;
+}
 
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1)
@@ -138,8 +149,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       uint32_t it = 0;
       bool ok = true;
       for (int tile = pair; tile < total && ok; tile += pairs) {
-        const int m0 = (tile % m_tiles) * 2 * C::BM + static_cast<int>(rank) * C::BM;
-        const int n0 = (tile / m_tiles) * BN + static_cast<int>(rank) * C::BH;
+        int tm, tn;
+        fp8_tile_at(tile, m_tiles, n_tiles, p.m_group, tm, tn);
+        const int m0 = tm * 2 * C::BM + static_cast<int>(rank) * C::BM;
+        const int n0 = tn * BN + static_cast<int>(rank) * C::BH;
         for (int kb = 0; kb < nkb; ++kb, ++it) {
           const int s = it % STAGES;
           if (!mbar_wait(smem_u32(&empty[s]), ((it / STAGES) & 1) ^ 1, abort_flag, p.status)) { ok = false; break; }
@@ -201,8 +214,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     const uint32_t res_bar = smem_u32(&res_full[ew]);
     uint32_t loads = 0, used = 0;  // residual fills asked for and waited for
     auto load_residual = [&](int tile) {
-      const int row0 = (tile % m_tiles) * 2 * C::BM + static_cast<int>(rank) * C::BM + q * 32;
-      const int n0 = (tile / m_tiles) * BN + h * C::HALF;
+      int tm, tn;
+      fp8_tile_at(tile, m_tiles, n_tiles, p.m_group, tm, tn);
+      const int row0 = tm * 2 * C::BM + static_cast<int>(rank) * C::BM + q * 32;
+      const int n0 = tn * BN + h * C::HALF;
       if (lane == 0) {
         mbar_arrive_expect_tx(res_bar, C::BOXES * C::BOX_BYTES);
 #pragma unroll
@@ -214,8 +229,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     if (p.R != nullptr && pair < total) load_residual(pair);
     uint32_t tcount = 0;
     for (int tile = pair; tile < total; tile += pairs, ++tcount) {
-      const int row0 = (tile % m_tiles) * 2 * C::BM + static_cast<int>(rank) * C::BM + q * 32;
-      const int n0 = (tile / m_tiles) * BN + h * C::HALF;
+      int tm, tn;
+      fp8_tile_at(tile, m_tiles, n_tiles, p.m_group, tm, tn);
+      const int row0 = tm * 2 * C::BM + static_cast<int>(rank) * C::BM + q * 32;
+      const int n0 = tn * BN + h * C::HALF;
       const uint32_t acc = tcount % C::NUM_ACC;
       // (rows past M read the last row's scale; the store drops their outputs)
       const float sa = __ldg(p.s_a + static_cast<int64_t>(min(row0 + lane, p.M - 1)) * p.s_a_step);

@@ -229,9 +229,11 @@ def test_linear_exact_sums(w4, M, N, K, gelu, bias, residual):
     assert np.all(err <= bound), (np.max(err / bound), np.unravel_index(np.argmax(err / bound), err.shape))
 
 
-@pytest.mark.parametrize("M,N,K", [(1100, 2312, 4112), (1000, 9400, 2064), (2000, 9400, 2064)])
+@pytest.mark.parametrize("M,N,K", [(1100, 2312, 4112), (1000, 9400, 2064), (2000, 9400, 2064),
+                                   (1100, 520, 65536), (300, 264, 131072)])
 def test_linear_wide_tiles(w4, M, N, K):
-    """256-column tiles: one, two and four a CTA pair, ragged on both sides."""
+    """256-column tiles: one, two and four a CTA pair, ragged on both sides;
+    rows so long that the row tiles are swept in groups of two and one."""
     g = rng(M + N)
     a, s_a, w, s_w, b, r = integer_case(g, M, N, K, True, True)
     A = w4.Fp8Rows(dev_u8(a), to_dev_f32(s_a))
