@@ -226,6 +226,23 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       }
       ++loads;
     };
+    // Scales and biases of 32 columns (the same for every lane), asked for a
+    // box ahead: under the products, then under the previous box's stores.
+    // (columns past N read the last ones'; the store drops their outputs)
+    float4 sw[8];
+    uint4 bw[4] = {};
+    auto load_columns = [&](int n) {
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const float4* w = reinterpret_cast<const float4*>(p.s_w + min(n + 8 * g, p.N - 8));
+        sw[2 * g] = __ldg(w);
+        sw[2 * g + 1] = __ldg(w + 1);
+      }
+      if (p.bias != nullptr) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) bw[g] = __ldg(reinterpret_cast<const uint4*>(p.bias + min(n + 8 * g, p.N - 8)));
+      }
+    };
     if (p.R != nullptr && pair < total) load_residual(pair);
     uint32_t tcount = 0;
     for (int tile = pair; tile < total; tile += pairs, ++tcount) {
@@ -236,6 +253,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       const uint32_t acc = tcount % C::NUM_ACC;
       // (rows past M read the last row's scale; the store drops their outputs)
       const float sa = __ldg(p.s_a + static_cast<int64_t>(min(row0 + lane, p.M - 1)) * p.s_a_step);
+      load_columns(n0);
       if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&acc_full[acc]), (tcount / C::NUM_ACC) & 1, abort_flag,
                                              p.status)))
         break;
@@ -261,46 +279,38 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
         uint8_t* box = boxes + c * C::BOX_BYTES;
         const int n = n0 + 32 * c;
+        float y[32];
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int col = n + 8 * g;
-          uint4* slot = reinterpret_cast<uint4*>(box + lane * 64 + ((g ^ ((lane >> 1) & 3)) << 4));
-          float sw[8], y[8];
-          if (col < p.N) {  // N % 8 == 0: all eight columns are valid
-            const float4 w0 = __ldg(reinterpret_cast<const float4*>(p.s_w + col));
-            const float4 w1 = __ldg(reinterpret_cast<const float4*>(p.s_w + col) + 1);
-            sw[0] = w0.x; sw[1] = w0.y; sw[2] = w0.z; sw[3] = w0.w;
-            sw[4] = w1.x; sw[5] = w1.y; sw[6] = w1.z; sw[7] = w1.w;
-          } else {
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t b0 = j & 1 ? bw[j >> 1].z : bw[j >> 1].x, b1 = j & 1 ? bw[j >> 1].w : bw[j >> 1].y;
+          y[4 * j] = fmaf(__uint_as_float(r[4 * j]) * sa, sw[j].x, bf16_lo(b0));
+          y[4 * j + 1] = fmaf(__uint_as_float(r[4 * j + 1]) * sa, sw[j].y, bf16_hi(b0));
+          y[4 * j + 2] = fmaf(__uint_as_float(r[4 * j + 2]) * sa, sw[j].z, bf16_lo(b1));
+          y[4 * j + 3] = fmaf(__uint_as_float(r[4 * j + 3]) * sa, sw[j].w, bf16_hi(b1));
+        }
+        if (c + 1 < C::BOXES) load_columns(n + 32);
+        if (p.epi == 1) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sw[j] = 0.0f;
-          }
-          uint32_t b[4] = {0u, 0u, 0u, 0u};
-          if (p.bias != nullptr && col < p.N) {
-            const uint4 bw = __ldg(reinterpret_cast<const uint4*>(p.bias + col));
-            b[0] = bw.x; b[1] = bw.y; b[2] = bw.z; b[3] = bw.w;
-          }
+          for (int j = 0; j < 32; ++j) y[j] = gelu_tanh_f32(y[j]);
+        }
+        uint4* line = reinterpret_cast<uint4*>(box + lane * 64);
+        const int flip = (lane >> 1) & 3;  // the box's 64-byte swizzle
+        if (p.R != nullptr) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float bj = (j & 1) ? bf16_hi(b[j >> 1]) : bf16_lo(b[j >> 1]);
-            y[j] = fmaf(__uint_as_float(r[8 * g + j]) * sa, sw[j], bj);
-          }
-          if (p.epi == 1) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = gelu_tanh_f32(y[j]);
-          }
-          if (p.R != nullptr) {
-            const uint4 rr = *slot;
+          for (int g = 0; g < 4; ++g) {
+            const uint4 rr = line[g ^ flip];
             const uint32_t rs[4] = {rr.x, rr.y, rr.z, rr.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              y[2 * j] += bf16_lo(rs[j]);
-              y[2 * j + 1] += bf16_hi(rs[j]);
+              y[8 * g + 2 * j] += bf16_lo(rs[j]);
+              y[8 * g + 2 * j + 1] += bf16_hi(rs[j]);
             }
           }
-          *slot = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
-                             pack_bf16x2(y[6], y[7]));
         }
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          line[g ^ flip] = make_uint4(pack_bf16x2(y[8 * g], y[8 * g + 1]), pack_bf16x2(y[8 * g + 2], y[8 * g + 3]),
+                                      pack_bf16x2(y[8 * g + 4], y[8 * g + 5]), pack_bf16x2(y[8 * g + 6], y[8 * g + 7]));
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -432,6 +442,14 @@ __global__ void __launch_bounds__(C::THREADS, 2)
     if (elect_one()) tc_commit(smem_u32(done));  // completes once every MMA above has, abort or not
   }
   __syncwarp();
+  // the outputs' column scales and biases (four weight rows a lane), under the products
+  const int n = n0 + 4 * lane;
+  float4 sw = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  uint2 bw = make_uint2(0u, 0u);
+  if (n < p.N) {  // N % 8 == 0: all four are valid
+    sw = __ldg(reinterpret_cast<const float4*>(p.s_w + n));
+    if (p.bias != nullptr) bw = __ldg(reinterpret_cast<const uint2*>(p.bias + n));
+  }
   const bool ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(done), 0, abort_flag, p.status));
   if (!ok) mbar_wait_drain(smem_u32(done), 0);
   tc_fence_after();
@@ -451,11 +469,7 @@ __global__ void __launch_bounds__(C::THREADS, 2)
   // Outputs: a token per warp, four weight rows a lane.  Two tokens at a time,
   // all their partial sums asked for before the first is added (one load
   // after the other, a row a thread, took 128 tokens 12 us).
-  const int n = n0 + 4 * lane;
-  if (ok && n < p.N) {  // N % 8 == 0: all four are valid
-    const float4 sw = __ldg(reinterpret_cast<const float4*>(p.s_w + n));
-    uint2 bw = make_uint2(0u, 0u);
-    if (p.bias != nullptr) bw = __ldg(reinterpret_cast<const uint2*>(p.bias + n));
+  if (ok && n < p.N) {
     const uint32_t mine = smem_u32(part + 4 * lane);
     const int stride = 4 * splits;  // tokens from one of a warp's to its next
     for (int m0 = split + warp * splits; m0 < p.M; m0 += 2 * stride) {
