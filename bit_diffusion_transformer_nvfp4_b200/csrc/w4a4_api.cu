@@ -785,31 +785,34 @@ int fp8_small_splits(int64_t n_tiles, int64_t k_steps, int64_t sms) {
 }
 
 // Which FP8 kernel a product takes, by its time on one B200 in units of 10 ns,
-// fitted to products of 1 to 9216 rows, 640 to 18432 columns and K from 512
-// to 8192 (most within 15 %).  Pairs: waves of tiles times K steps times the
-// step (256 x 64, 128 and 256 tiles: 0.20, 0.25, 0.41 us), and a beginning and
-// end.  Few rows: the K steps of a slice, dearer with more tokens a tile and
-// with more than one CTA on an SM, and the exchange of the partial sums.
-// Measured on both sides: 128 x 9216 x 3200 16.4 us by the weight, 12.4 by
-// pairs; 64 x 18432 x 6144 25.4 and 31.0; 333 x 2056 x 4112 13.1, 16.0 and 19.9
-// with tiles 64, 128 and 256 wide, 640 x 6144 x 6144 40.6, 28.3 and 26.0.
+// fitted to products of 24 to 9216 rows, 280 to 18432 columns and K from 512
+// to 8192 (most within 10 %).  Pairs: a beginning and end, and waves of tiles,
+// each of its K steps or, where K is short, of the tile's epilogue.  Few rows:
+// the K steps of a slice, dearer with more tokens a tile and with more than
+// one CTA on an SM, and the exchange of the partial sums.
+// Measured on both sides: 64 x 18432 x 6144 25.7 us by the weight, 27.5 by
+// pairs, 100 x 9216 x 3200 13.3 and 10.6; 333 x 2056 x 4112 13.4, 15.4 and 18.8
+// with tiles 64, 128 and 256 wide, 9216 x 640 x 512 11.3, 10.3 and 10.3, 640 x
+// 6144 x 6144 40.8, 27.7 and 25.0, 1729 x 4528 x 1536 23.0, 18.5 and 14.5.
 // Returns 0 for the kernel for few rows, else the tile width.
 int fp8_gemm_plan(int64_t M, int64_t N, int64_t K, int64_t sms) {
   const int64_t k_steps = ceil_div(K, 128), n_tiles = ceil_div(N, 128);
   int best = 256;
   int64_t cost = INT64_MAX;
-  const int width[3] = {64, 128, 256}, step[3] = {20, 25, 41}, ends[3] = {350, 450, 700};
+  const int width[3] = {64, 128, 256}, ends[3] = {508, 498, 542}, step[3] = {19, 24, 37}, epilogue[3] = {131, 210, 343};
   for (int i = 0; i < 3; ++i) {
     const int64_t waves = ceil_div(ceil_div(M, 256) * ceil_div(N, width[i]), sms / 2);
-    const int64_t c = waves * k_steps * step[i] + ends[i];
+    const int64_t c = ends[i] + waves * std::max<int64_t>(k_steps * step[i], epilogue[i]);
     if (c < cost) {
       cost = c;
       best = width[i];
     }
   }
   if (M <= 128 && n_tiles <= 65535) {
-    const int s = fp8_small_splits(n_tiles, k_steps, sms);
-    const int64_t c = 480 + 340 * M / 128 + ceil_div(k_steps, s) * (26 + 35 * M / 128) * std::max(n_tiles * s, sms) / sms;
+    const int64_t ctas = n_tiles * fp8_small_splits(n_tiles, k_steps, sms);
+    const int64_t steps = ceil_div(k_steps * n_tiles, ctas);
+    const int64_t c = 500 + 460 * M / 128 + steps * (19 + 11 * M / 128) * std::max(ctas, sms) / sms +
+                      910 * M / 128 * std::max<int64_t>(ctas - sms, 0) / sms;
     if (M <= 16 || c < cost) best = 0;
   }
   return best;
