@@ -12,8 +12,8 @@
 // from one pass and one reduction, and the row stays in registers: every
 // input is read once and every output written once.  That traffic (for
 // x, r, hidden and codes 7 bytes an element) is the bound: norm of 16896 x
-// 6144 108 us (6.7 TB/s), its codes alone 46.3 us (6.7 TB/s).  Rows of a few
-// hundred columns are bound by instruction issue (100000 x 256: 3.6 TB/s).
+// 6144 109 us (6.7 TB/s), its codes alone 46.3 us (6.7 TB/s).  Short rows are
+// bound by instruction issue (36888 x 128 without a residual: 3.7 us, 3.8 TB/s).
 //
 // Two shapes: rows of up to 2048 columns take a power of two of lanes of one
 // warp (shuffles only); wider ones a block of their own, a thread holding V
@@ -122,19 +122,29 @@ __device__ __forceinline__ RowStats rows_take(const RowsFp8Params& p, int64_t ro
 // The row's factor and scale, then this thread's outputs.
 template <int V, bool NORM>
 __device__ __forceinline__ void rows_store(const RowsFp8Params& p, int64_t row, int t0, int step, bool first,
-                                           RowStats st, const float (&v)[8 * V]) {
+                                           RowStats st, float (&v)[8 * V]) {
   const int nv = p.cols >> 3;
   // the norm's factor and quotients by the hardware's reciprocals (a few
   // units of the 23rd bit; the plain codes' are exact divisions, whose steps
   // their definition fixes): every lane of a short row does these
-  const float inv = NORM ? rsqrtf(fmaf(st.sum, p.inv_cols, p.eps)) : 1.0f;
+  float inv = NORM ? rsqrtf(fmaf(st.sum, p.inv_cols, p.eps)) : 1.0f;
+  if (NORM && !(st.top >= 0x1p-118f && st.top <= 0x1p125f)) {
+    // 448 / max|v| would leave fp32's range or __fdividef's: the factor first,
+    // and 1 / s below
+#pragma unroll
+    for (int i = 0; i < 8 * V; ++i) v[i] *= inv;
+    st.top *= inv;
+    inv = 1.0f;
+  }
   if (p.codes != nullptr) {
     float s = NORM ? st.top * inv * (1.0f / 448.0f) : st.top / 448.0f;
     const bool normal = s >= 1.17549435e-38f && s < INFINITY;
     if (!normal) s = 1.0f;
     if (first) p.scales[row] = s;
     // (i / s = 448 / max|v|)
-    const float f = !normal ? inv : NORM ? __fdividef(448.0f, st.top) : 1.0f / s;
+    const float f = !normal ? inv
+                    : NORM  ? __fdividef(inv != 1.0f ? 448.0f : 1.0f, inv != 1.0f ? st.top : s)
+                            : 1.0f / s;
     uint2* out = reinterpret_cast<uint2*>(p.codes + row * p.ldo);
 #pragma unroll
     for (int i = 0; i < V; ++i) {

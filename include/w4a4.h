@@ -441,6 +441,8 @@ int fp8_quantize_rows(const void* X, int64_t rows, int64_t cols, int64_t ldx, ui
  *   codes, scales  out as in fp8_quantize_rows; codes NULL: neither is
  *                 written (then normed must be given)
  * Sizes and strides as in fp8_quantize_rows.  A zero row with eps 0 is NaN.
+ * sum(h^2) and h * weight are fp32: where the sum overflows (|h| from about
+ * 1e19) y is 0, where only the product does, infinite.
  */
 int rmsnorm_fp8(const void* X, int64_t rows, int64_t cols, int64_t ldx, const void* R, int64_t ldr,
                 const void* weight, float eps, void* hidden, int64_t ldh, void* normed, int64_t ldn,
@@ -482,7 +484,8 @@ int fp8_gemm(const uint8_t* A8, int64_t lda, const float* s_a, int s_a_rows, int
  *   softmax_scale  c (normally 1/sqrt(d_head)), > 0 and < 2.3e38
  *   O     out bf16 [batch * Sq, ldo]
  * Keys that do not count may hold anything, NaN included.  A query without a
- * key gets 0.  A counted score that is NaN or +infinity makes its row NaN.
+ * key gets 0.  A counted score that is NaN or +infinity makes its row NaN;
+ * one of -infinity weighs nothing (a row of nothing else is 0).
  * fp32 scores, sums and accumulation; the probabilities are rounded to bf16
  * for the second product.  Strides are in elements, multiples of 8 (ld_mask:
  * any, >= Skv); Sq, Skv <= 2^24, batch and heads <= 65535, batch * heads *

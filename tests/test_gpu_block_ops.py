@@ -163,6 +163,19 @@ def test_norm_in_place_and_without_codes(w4):
         np.testing.assert_allclose(from_dev_bf16(Y), oblock.rms_norm(x, eps=1e-5)[1], rtol=BF16 + NORM)
 
 
+def test_norm_of_extreme_products(w4):
+    """h * weight near either end of fp32, the norm itself well inside."""
+    g = rng(83)
+    for cols in (264, 2056):
+        for top, scale, eps in ((2.0 ** 30, 2.0 ** 95, 1e-6), (2.0 ** -34, 2.0 ** -90, 0.0)):
+            h = bf16_round((g.uniform(1.0, 2.0, (4, cols)) * g.choice([-top, top], (4, cols))).astype(np.float32))
+            w = bf16_round((g.uniform(1.0, 2.0, cols) * scale).astype(np.float32))
+            a, _ = w4.rms_norm_fp8(to_dev_bf16(h), to_dev_bf16(w), eps=eps)
+            y = oblock.rms_norm(h, None, w, eps)[1]
+            check_codes(a, y)
+            assert np.all(np.abs(y) > 0) and a.codes.cpu().numpy().any(axis=1).all()
+
+
 def test_norm_of_zero_rows_and_large_offsets(w4):
     """A zero row gives zeros and scale 1; rows beyond 2^31 elements are found."""
     import torch
@@ -418,6 +431,26 @@ def test_cross_attention_moves_its_offset(w4, sq):
     k[450, 0] = 80.0
     O = w4.cross_attention(to_dev_bf16(q), to_dev_bf16(k), to_dev_bf16(v), heads=2)
     check_attention(from_dev_bf16(O), *oblock.cross_attention(q, k, v, 2, 2, 1, 1))
+
+
+@pytest.mark.parametrize("sq", [4, 400])
+def test_cross_attention_scores_of_minus_infinity(w4, sq):
+    """Scores that overflow below weigh nothing, over a whole tile too; a row
+    of nothing else is 0."""
+    g = rng(29 + sq)
+    sk, d = 400, 64
+    q, k, v = attention_case(g, 1, 1, sq, sk, 2, 2, d)
+    q[:, 0] = 2.0 ** 70
+    gone = g.random(sk) < 0.4
+    gone[:130] = True
+    k[:, 0] = np.where(gone, -2.0 ** 70, 0.0)
+    O = from_dev_bf16(w4.cross_attention(to_dev_bf16(q), to_dev_bf16(k), to_dev_bf16(v), heads=2))
+    want, avg = oblock.cross_attention(q, k, v, 2, 2, 1, 1)
+    check_attention(O, want, avg)
+    k[:, 0] = -2.0 ** 70
+    O = from_dev_bf16(w4.cross_attention(to_dev_bf16(q), to_dev_bf16(k), to_dev_bf16(v), heads=2))
+    assert not O[:, :d].any()
+    check_attention(O[:, d:], want[:, d:], avg[:, d:])
 
 
 @pytest.mark.parametrize("sq", [4, 400])
