@@ -807,7 +807,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
       }
     }
     tc_fence_before();
-    cluster_sync();  // the peers have read this CTA's sums
+    cluster_meet();  // the peers have read this CTA's sums
   } else {
     tc_fence_before();
     __syncthreads();

@@ -203,6 +203,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       if (elect_one()) tc_commit_pair(smem_u32(drain));
       __syncwarp();
       mbar_wait_drain(smem_u32(drain), 0);
+      // the other CTA's last arrivals are in before this one may go
+      for (uint32_t t = tcount > C::NUM_ACC ? tcount - C::NUM_ACC : 0u; ok && t < tcount; ++t)
+        ok = mbar_wait_warp(smem_u32(&acc_empty[t % C::NUM_ACC]), (t / C::NUM_ACC) & 1, abort_flag, p.status);
     }
   } else if (warp >= C::EPI_WARP0) {
     // ------------------------------------------------------------ epilogue (both CTAs)
@@ -333,7 +336,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   }
 
   tc_fence_before();
-  cluster_sync();  // no CTA leaves while its peer may still signal it or read its TMEM
+  cluster_meet();  // no CTA leaves while its peer may still signal it or read its TMEM
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, C::TMEM_COLS);
@@ -515,7 +518,7 @@ __global__ void __launch_bounds__(C::THREADS, 2)
     }
   }
   tc_fence_before();
-  cluster_sync();  // the peers have read this CTA's partial sums
+  cluster_meet();  // the peers have read this CTA's partial sums
   if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tmem, C::TMEM_COLS);
