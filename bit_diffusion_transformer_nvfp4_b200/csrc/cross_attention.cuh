@@ -653,21 +653,24 @@ __global__ void __launch_bounds__(kXThreads, 1)
         stat[kXTile + r] = l;
         float* part = reinterpret_cast<float*>(smem) + (t * kXTile + r) * C::PART_PITCH;
         const bool live = a.row0 + r < p.Sq * p.pack;
+        if (__any_sync(0xffffffffu, live)) {
 #pragma unroll 1
-        for (int cc = 0; cc < DB * 4; ++cc) {
-          uint32_t v[16];
-          if (some) {
-            tmem_ld_16cols(t_o + 16 * cc, v);
-            tmem_ld_wait();
-          } else {
+          for (int cc = 0; cc < DB; ++cc) {
+            uint32_t v[64];
+            if (some) {
+              tmem_ld_32cols(t_o + 64 * cc, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
+              tmem_ld_32cols(t_o + 64 * cc + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
+              tmem_ld_wait();
+            } else {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = 0u;
-          }
-          if (live) {
+              for (int e = 0; e < 64; ++e) v[e] = 0u;
+            }
+            if (live) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              *reinterpret_cast<uint4*>(part + 16 * cc + 4 * e) =
-                  make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+              for (int e = 0; e < 16; ++e)
+                *reinterpret_cast<uint4*>(part + 64 * cc + 4 * e) =
+                    make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+            }
           }
         }
       } else {
@@ -756,29 +759,18 @@ __global__ void __launch_bounds__(kXThreads, 1)
   if constexpr (SPLIT) {
     cluster_sync();  // every CTA's partial sums are in its shared memory
     if (warp >= 4 && warp < 12 && first < p.tiles && *abort_flag == 0) {
-      // rows of the tile times groups of four columns, shared out over the cluster
+      // rows of the tile times groups of four columns, shared out evenly over the cluster
       const XTileAt a = XWalk(p, first).at(p, kRows);
-      const int rows = min(kXTile, p.Sq * p.pack - a.row0), groups = p.D / 4;
+      const int groups = p.D / 4, total = min(kXTile, p.Sq * p.pack - a.row0) * groups;
+      const int end = total * (split + 1) / splits;
       const uint32_t part0 = smem_u32(smem), stat0 = smem_u32(smem + C::STAT_OFF);
-      for (int e = split * 256 + threadIdx.x - 128; e < rows * groups; e += splits * 256) {
+      for (int e = total * split / splits + threadIdx.x - 128; e < end; e += 256) {
         const int row = e / groups, g = e % groups;
-        // every stream of every CTA: all offsets, then sums and columns, asked
-        // for before the first is used
-        float ms[16], m = -INFINITY;
-#pragma unroll
-        for (int s = 0; s < 16; ++s)
-          ms[s] = s < 2 * splits
-                      ? ld_cluster_f32(mapa_shared(stat0 + 4u * ((s & 1) * 2 * kXTile + row), s >> 1))
-                      : -INFINITY;
-#pragma unroll
-        for (int s = 0; s < 16; ++s) m = fmaxf(m, ms[s]);
-        float l = 0.0f;
-        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-        for (int s0 = 0; s0 < 16; s0 += 8) {
-          if (s0 >= 2 * splits) break;
-          float ls[8];
-          float4 v[8];
+        // every stream of every CTA: all offsets, and eight streams' sums and
+        // columns at a time, asked for before the first is used
+        float ms[16], ls[8], m = -INFINITY, l = 0.0f;
+        float4 v[8], o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        auto fetch = [&](int s0) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int s = s0 + i;
@@ -790,6 +782,8 @@ __global__ void __launch_bounds__(kXThreads, 1)
                   mapa_shared(part0 + 4u * (((s & 1) * kXTile + row) * C::PART_PITCH + 4 * g), s >> 1));
             }
           }
+        };
+        auto add = [&](int s0) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const float w = ms[s0 + i] == m ? 1.0f : ex2_approx(ms[s0 + i] - m);
@@ -799,6 +793,19 @@ __global__ void __launch_bounds__(kXThreads, 1)
             o.z = fmaf(w, v[i].z, o.z);
             o.w = fmaf(w, v[i].w, o.w);
           }
+        };
+#pragma unroll
+        for (int s = 0; s < 16; ++s)
+          ms[s] = s < 2 * splits
+                      ? ld_cluster_f32(mapa_shared(stat0 + 4u * ((s & 1) * 2 * kXTile + row), s >> 1))
+                      : -INFINITY;
+        fetch(0);
+#pragma unroll
+        for (int s = 0; s < 16; ++s) m = fmaxf(m, ms[s]);
+        add(0);
+        if (splits > 4) {
+          fetch(8);
+          add(8);
         }
         const float f = xattn_factor(m, l);
         const int token = (a.row0 + row) / p.pack, head = a.h0 + (a.row0 + row) % p.pack;
