@@ -8,14 +8,17 @@
 //
 // Two kernels:
 //   gemm_fp8_pair_kernel   many rows: persistent CTA pairs, 256 x BN tiles.
-//                          Bound by the FP8 tensor pipe (79 % active under
-//                          ncu) and its power: 4608 x 6144 x 6144 119 us (2920
-//                          TFLOP/s) a few at a time, 148 us in a long run.
+//                          Bound by the FP8 tensor pipe (81 % active under
+//                          ncu) and its power: 4608 x 6144 x 6144 118 us (2940
+//                          TFLOP/s) a few at a time, 145 us in a long run.
+//                          One wave of tiles is bound by L2, some 50 bytes a
+//                          cycle and SM (256 x 256: 625 cycles a K step of
+//                          512 in the pipe), and by 5 us of beginning and end.
 //   gemm_fp8_small_kernel  few rows: bound by streaming the weight once, so
 //                          the weight rows are the 128-row operand, the
 //                          tokens the narrow one, K is split over a cluster
 //                          and the partial sums meet in shared memory.  One
-//                          token times 36864 x 6144: 38.7 us, 5.85 TB/s.
+//                          token times 36864 x 6144: 38.2 us, 5.93 TB/s.
 #pragma once
 
 #include "attention.cuh"
@@ -230,7 +233,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       ++loads;
     };
     // Scales and biases of 32 columns (the same for every lane), asked for a
-    // box ahead: under the products, then under the previous box's stores.
+    // box ahead: under the products, then under the previous box's stores
+    // (asked for where they are used, each group of eight waits for L2: 2000
+    // cycles a box; handed round by shuffles 950; this way 570).
     // (columns past N read the last ones'; the store drops their outputs)
     float4 sw[8];
     uint4 bw[4] = {};

@@ -873,8 +873,8 @@ bool encode_heads(CUtensorMap* m, const void* ptr, int64_t D, int64_t heads, int
 // key tile and 3 us a work tile, one after the other on an SM.  Split: 7 us
 // and 1.4 us a key tile, in waves of the clusters that are resident at once
 // (B200: 74 of two, 33 of four, 15 of eight).
-// Measured: 4 x 1 query, 4109 keys, 32 heads on 8: 18.8 us in fours; 1 query,
-// 4096 keys, 16 heads: 21.5 us in eights (two waves of clusters).
+// Measured: 4 x 1 query, 4109 keys, 32 heads on 8: 17.5 us in fours; 1 query,
+// 4096 keys, 16 heads: 12.8 us in one wave of clusters, 21.5 in two of eights.
 int xattn_splits(int64_t rows, int64_t head_blocks, int64_t key_tiles, const DeviceInfo& dev) {
   int best = 0;
   int64_t cost = ceil_div(ceil_div(rows, 2 * kXTile) * head_blocks, dev.num_sms) * (17 * key_tiles + 30) + 30;
