@@ -526,25 +526,28 @@ __global__ void __launch_bounds__(kXThreads, 1)
         if ((keep[0] & keep[1]) != 0xffffffffu) {
           // The values of keys that do not count may hold anything (0 times
           // NaN is NaN): cleared once the tile has landed and before this
-          // stream's probabilities let its product start.  Streams that
-          // share a value tile both do it (the second writes zeros over
-          // zeros).
-          const uint32_t i = u >> 1;
-          const uint32_t v = SPLIT ? (i + 1 < static_cast<uint32_t>(n) ? 2 * i + 2 : 2 * n - 1) : fills + 2 * i + 1;
-          if (!got(&kv_full[v % SLOTS], v / SLOTS)) {
-            ok = false;
-            break;
-          }
-          // two threads a key, each half of its columns (in an order that
-          // spreads the lanes' rows over the banks)
-          if (!((q & 1 ? keep[1] : keep[0]) >> lane & 1)) {
-            uint8_t* row = smem + C::KV_OFF + (v % SLOTS) * C::TILE_BYTES + (kXSub * h + (r & 63)) * 128 +
-                           (r >> 6) * (DB == 2 ? kXTile * 128 : 64);
+          // stream's probabilities let its product start, two threads a key
+          // with half of its columns each.  (Past the last key of all, TMA
+          // has filled zeros.)  Streams that share a value tile both do it
+          // (the second writes zeros over zeros).
+          const bool clear = !((q & 1 ? keep[1] : keep[0]) >> lane & 1) && key0 + (r & 63) < p.Skv;
+          if (__any_sync(0xffffffffu, clear)) {
+            const uint32_t i = u >> 1;
+            const uint32_t v = SPLIT ? (i + 1 < static_cast<uint32_t>(n) ? 2 * i + 2 : 2 * n - 1) : fills + 2 * i + 1;
+            if (!got(&kv_full[v % SLOTS], v / SLOTS)) {
+              ok = false;
+              break;
+            }
+            if (clear) {
+              uint8_t* row = smem + C::KV_OFF + (v % SLOTS) * C::TILE_BYTES + (kXSub * h + (r & 63)) * 128 +
+                             (r >> 6) * (DB == 2 ? kXTile * 128 : 64);
+              // (in an order that spreads the lanes' rows over the banks)
 #pragma unroll
-            for (int e = 0; e < 4 * DB; ++e)
-              *reinterpret_cast<uint4*>(row + 16 * ((e ^ lane) & (4 * DB - 1))) = make_uint4(0u, 0u, 0u, 0u);
+              for (int e = 0; e < 4 * DB; ++e)
+                *reinterpret_cast<uint4*>(row + 16 * ((e ^ lane) & (4 * DB - 1))) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
           }
-          fence_proxy_async_smem();
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
             if (!(keep[0] >> e & 1)) sv[e] = 0xff800000u;  // -inf: no weight
