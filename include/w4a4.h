@@ -460,9 +460,9 @@ int rmsnorm_fp8(const void* X, int64_t rows, int64_t cols, int64_t ldx, const vo
  *            and stride)
  *   Y    out bf16 [M, ldy]
  *   K % 16 == 0, K <= W4A4_MAX_K, N % 8 == 0, lda / ldw % 16 == 0, ldr / ldy % 8 == 0
- * Up to 128 rows: the weight streams past the tokens, K split over a cluster
- * of CTAs whose partial sums are added in slice order (deterministic); more:
- * CTA pairs with 256-row tiles.
+ * Up to 16 rows, and up to 128 where it is faster: the weight streams past the
+ * tokens, K split over a cluster of CTAs whose partial sums are added in slice
+ * order; more: CTA pairs with 256-row tiles.  Results do not depend on timing.
  */
 int fp8_gemm(const uint8_t* A8, int64_t lda, const float* s_a, int s_a_rows, int64_t M, int64_t N, int64_t K,
              const uint8_t* W8, int64_t ldw, const float* s_w, const void* bias, int epilogue, const void* R,
