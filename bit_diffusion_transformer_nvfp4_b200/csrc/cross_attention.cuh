@@ -6,9 +6,12 @@
 // c = scale log2 e, the sums and the running offset m in fp32; a row without
 // keys gives 0.  m moves only when a half tile's maximum passes it by more
 // than kXSlack binades (the accumulator and the sum are then rescaled), which
-// is exact: numerator and denominator share the offset.  The probabilities
-// are rounded to bf16 for the second product, at most 2^-8 each, random in
-// sign, against the same bound of the output's own rounding.
+// is exact: numerator and denominator share the offset, the rounded product of
+// c and the largest score.  Where that rounding would be a binade (from |m| =
+// kXLarge up) the exponents are c times the scores' differences instead
+// (xattn_ahead).  The probabilities are rounded to bf16 for the second product,
+// at most 2^-8 each, random in sign, against the same bound of the output's own
+// rounding.
 //
 // A work tile is 128 rows of one key/value head: queries times the heads that
 // share it (the largest power of two of them, so that a group of heads reads
@@ -57,6 +60,7 @@ constexpr int kXTile = 128;       // rows per stream, keys of a ring slot
 constexpr int kXSub = 64;         // keys of a score buffer
 constexpr int kXThreads = 512;    // control warpgroup, a softmax warpgroup a stream, epilogue warpgroup
 constexpr float kXSlack = 8.0f;   // binades a tile's maximum may pass the offset
+constexpr float kXLarge = 0x1p24f;  // offsets up to here are rounded (by half a binade at most)
 constexpr int kXChunk = 16;       // scores taken together through the exponential
 // Of 16 pairs of exponentials, how many on the FMA pipes instead of the MUFU
 // (0, 2, 4 and 6: 443, 427, 425 and 428 us on the long case; fewer take less power).
@@ -95,7 +99,7 @@ struct XAttnCfg {
   static constexpr int O_OFF = KV_OFF + SLOTS * TILE_BYTES;
   static constexpr int O_BYTES = SPLIT ? 0 : 8 * 32 * 128;       // two 32 x 64 bf16 boxes per epilogue warp
   static constexpr int PART_PITCH = DB * 64 + 4;                 // floats; SPLIT: over Q and the ring
-  static constexpr int STAT_OFF = 2 * kXTile * PART_PITCH * 4;   // behind them m and l, [2 streams][2][128]
+  static constexpr int STAT_OFF = 2 * kXTile * PART_PITCH * 4;   // behind them m, l and x, [2 streams][3][128]
   static constexpr int F_OFF = O_OFF + O_BYTES;                  // the rows' final factors, [2 streams][128]
   static constexpr int BAR_OFF = F_OFF + (SPLIT ? 0 : 2 * kXTile * 4);
   static constexpr int BARS = 2 * SLOTS + 2 * 10;
@@ -103,7 +107,7 @@ struct XAttnCfg {
   static constexpr int TMEM_COLS = 512;
   static constexpr int O_COL = 256;        // S of stream t at 128 t, O at 256 + 128 t
   static_assert(SMEM <= 232448, "shared memory budget");
-  static_assert(!SPLIT || STAT_OFF + 4 * kXTile * 4 <= O_OFF, "the partial sums fit over Q and the ring");
+  static_assert(!SPLIT || STAT_OFF + 6 * kXTile * 4 <= O_OFF, "the partial sums fit over Q and the ring");
 };
 
 // D(tmem) (+)= A(tmem) * B(smem), bf16 inputs, fp32 accumulate.
@@ -125,9 +129,22 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
 }
 
 // The factor of a row's sums at the end: 1 / l, 0 for a row without keys
-// (whose offset never moved), NaN where l is.
-__device__ __forceinline__ float xattn_factor(float m, float l) {
-  return m == -INFINITY && l == l ? 0.0f : 1.0f / l;
+// (whose largest score is still -infinity), NaN where l is.
+__device__ __forceinline__ float xattn_factor(float x, float l) {
+  return x == -INFINITY && l == l ? 0.0f : 1.0f / l;
+}
+
+// Offsets.  A row whose largest score is x has the offset m = c x, rounded to
+// fp32 up to kXLarge and taken as the exact product beyond: there its rounding
+// would be a binade and more, and 2^(c s - m) would leave fp32's range from
+// |m| = 2^31 on.
+__device__ __forceinline__ bool xattn_large(float m) { return !(fabsf(m) <= kXLarge); }
+
+// The offset of largest score a less that of b, rounded once.
+__device__ __forceinline__ float xattn_ahead(float a, float b, float c) {
+  const float ma = __fmul_rn(a, c), mb = __fmul_rn(b, c);  // (as the offsets were: never fused)
+  if (xattn_large(ma)) return xattn_large(mb) ? (a - b) * c : fmaf(a, c, -mb);
+  return xattn_large(mb) ? fmaf(-b, c, ma) : ma - mb;
 }
 
 // What a work tile index stands for.
@@ -495,24 +512,25 @@ __global__ void __launch_bounds__(kXThreads, 1)
       xattn_key_range(a.len, split, splits, j0, j1);
       const int n = j1 - j0;
       const bool some = SPLIT ? t < n : n > 0;  // this stream has keys here
-      float m_used = -INFINITY, l = 0.0f;  // offset (log2 domain) and sum of 2^(c s - offset)
+      // the offset (log2 domain), the score that it stands for, the sum of 2^(c s - offset)
+      float m_used = -INFINITY, x_used = -INFINITY, l = 0.0f;
       bool begun = false;
       // half key tiles (SPLIT: of every second key tile)
       for (int u = SPLIT ? 2 * t : 0; u < 2 * n; u += SPLIT && (u & 1) ? 3 : 1) {
         const int h = u & 1;
         const int key0 = j0 * kXTile + u * kXSub;
-        // the keys of this half that count, one bit each
-        uint32_t keep[2];
-#pragma unroll
-        for (int w32 = 0; w32 < 2; ++w32) {
-          const int left = a.len - (key0 + 32 * w32);
-          keep[w32] = left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1u;
+        // the keys of this half that count, one bit each, 32 from key0 + k on
+        auto counted = [&](int k) -> uint32_t {
+          const int left = a.len - (key0 + k);
+          uint32_t bits = left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1u;
           if (p.key_mask != nullptr) {
-            const int key = key0 + 32 * w32 + lane;
+            const int key = key0 + k + lane;
             const bool on = key < p.Skv && p.key_mask[static_cast<int64_t>(a.kb) * p.ld_mask + key] != 0;
-            keep[w32] &= __ballot_sync(0xffffffffu, on);
+            bits &= __ballot_sync(0xffffffffu, on);
           }
-        }
+          return bits;
+        };
+        const uint32_t keep[2] = {counted(0), counted(32)};
         const uint32_t t_buf = t_s + kXSub * h;
         if (!got(&s_full[2 * t + h], it)) {
           ok = false;
@@ -578,15 +596,19 @@ __global__ void __launch_bounds__(kXThreads, 1)
             mx[w] = max3_nan(mx[w], __uint_as_float(sv[e + w]), __uint_as_float(sv[e + w + 8]));
 #pragma unroll
         for (int e = 0; e < 8; ++e) mx[e] = max3_nan(mx[e], __uint_as_float(sv[56 + e]), mx[e]);
-        const float m_tile =
-            max3_nan(max3_nan(mx[0], mx[1], mx[2]), max3_nan(mx[3], mx[4], mx[5]), max3_nan(mx[6], mx[7], mx[7])) * c;
+        const float x_tile =
+            max3_nan(max3_nan(mx[0], mx[1], mx[2]), max3_nan(mx[3], mx[4], mx[5]), max3_nan(mx[6], mx[7], mx[7]));
         // a score that is NaN or +infinity makes its row NaN (the polynomial
         // below would drop it)
-        if (!(m_tile < INFINITY)) l = __int_as_float(0x7fffffff);
-        const bool moves = m_tile > m_used + kXSlack;
-        if (__any_sync(0xffffffffu, moves)) {
-          const float f = moves ? ex2_approx(m_used - m_tile) : 1.0f;
+        if (!(x_tile < INFINITY)) l = __int_as_float(0x7fffffff);
+        const float m_tile = __fmul_rn(x_tile, c);
+        if (__any_sync(0xffffffffu, m_tile > m_used + kXSlack || xattn_large(m_used))) {
+          // (two scores can differ by many binades under one rounded large offset)
+          const bool moves = m_tile > m_used + kXSlack || (xattn_large(m_used) && x_tile > x_used);
+          float f = 1.0f;
           if (moves) {
+            f = x_used == -INFINITY ? 0.0f : ex2_approx(xattn_ahead(x_used, x_tile, c));
+            x_used = x_tile;
             m_used = m_tile;
             l *= f;
           }
@@ -608,9 +630,45 @@ __global__ void __launch_bounds__(kXThreads, 1)
               tmem_st_16cols(t_o + 16 * cc, v);
             }
           }
+          if (__builtin_expect(__any_sync(0xffffffffu, x_used > -INFINITY && xattn_large(m_used)), 0)) {
+            // A large row: exponents from the scores' differences, in a loop of
+            // its own over the scores as they lie in TMEM (woven into the one
+            // below they cost every call a tenth).
+            const bool large = x_used > -INFINITY && xattn_large(m_used);
+            const float off = x_used == -INFINITY ? 0.0f : m_used;
+            float la = 0.0f, lb = 0.0f;
+#pragma unroll 1
+            for (int w32 = 0; w32 < 2; ++w32) {
+              uint32_t sw[32], bw[16];
+              tmem_ld_32cols(t_buf + 32 * w32, sw);
+              tmem_ld_wait();
+              const uint32_t on = counted(32 * w32);
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                float y[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  const float s = on >> (e + i) & 1 ? __uint_as_float(sw[e + i]) : -INFINITY;
+                  y[i] = ex2_approx(large ? (s - x_used) * c : fmaf(s, c, -off));
+                }
+                bw[e / 2] = pack_bf16x2(y[0], y[1]);
+                la += y[0];
+                lb += y[1];
+              }
+              tmem_st_16cols(t_buf + 16 * w32, bw);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&p_full[2 * t + h]));
+            l += la + lb;
+            begun = true;
+            it += h;
+            continue;
+          }
         }
         begun = true;
-        const float off = m_used == -INFINITY ? 0.0f : m_used;
+        const float off = x_used == -INFINITY ? 0.0f : m_used;
         float la = 0.0f, lb = 0.0f, lc = 0.0f, ld = 0.0f;
         uint32_t b[kXSub / 2];
 #pragma unroll
@@ -651,9 +709,10 @@ __global__ void __launch_bounds__(kXThreads, 1)
         // both streams' last products are done, the ring is read
         if ((some && !got(&o_done[t], 0)) || ((t == 0 ? n > 1 : n > 0) && !got(&o_done[t ^ 1], 0))) break;
         tc_fence_after();
-        float* stat = reinterpret_cast<float*>(smem + C::STAT_OFF) + 2 * kXTile * t;
-        stat[r] = m_used;
+        float* stat = reinterpret_cast<float*>(smem + C::STAT_OFF) + 3 * kXTile * t;
+        stat[r] = x_used > -INFINITY && xattn_large(m_used) ? __int_as_float(0x7fffffff) : m_used;  // NaN: see x
         stat[kXTile + r] = l;
+        stat[2 * kXTile + r] = x_used;
         float* part = reinterpret_cast<float*>(smem) + (t * kXTile + r) * C::PART_PITCH;
         const bool live = a.row0 + r < p.Sq * p.pack;
         if (__any_sync(0xffffffffu, live)) {
@@ -682,7 +741,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
         // tile before
         if (closed > 0 && !got(&o_free[t], closed - 1)) break;
         ++closed;
-        reinterpret_cast<float*>(smem + C::F_OFF)[t * kXTile + r] = xattn_factor(m_used, l);
+        reinterpret_cast<float*>(smem + C::F_OFF)[t * kXTile + r] = xattn_factor(x_used, l);
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&f_full[t]));
       }
@@ -771,7 +830,14 @@ __global__ void __launch_bounds__(kXThreads, 1)
         const int row = e / groups, g = e % groups;
         // every stream of every CTA: all offsets, and eight streams' sums and
         // columns at a time, asked for before the first is used
-        float ms[16], ls[8], m = -INFINITY, l = 0.0f;
+        auto stat = [&](int s, int i) {
+          return ld_cluster_f32(mapa_shared(stat0 + 4u * (((s & 1) * 3 + i) * kXTile + row), s >> 1));
+        };
+        auto cols = [&](int s) {
+          return ld_cluster_f32x4(
+              mapa_shared(part0 + 4u * (((s & 1) * kXTile + row) * C::PART_PITCH + 4 * g), s >> 1));
+        };
+        float ms[16], ls[8], m = -INFINITY, l = 0.0f, top;
         float4 v[8], o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         auto fetch = [&](int s0) {
 #pragma unroll
@@ -780,37 +846,46 @@ __global__ void __launch_bounds__(kXThreads, 1)
             ls[i] = 0.0f;
             v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             if (s < 2 * splits) {
-              ls[i] = ld_cluster_f32(mapa_shared(stat0 + 4u * ((s & 1) * 2 * kXTile + kXTile + row), s >> 1));
-              v[i] = ld_cluster_f32x4(
-                  mapa_shared(part0 + 4u * (((s & 1) * kXTile + row) * C::PART_PITCH + 4 * g), s >> 1));
+              ls[i] = stat(s, 1);
+              v[i] = cols(s);
             }
           }
         };
+        auto join = [&](float w, float ls, const float4& v) {
+          l = fmaf(w, ls, l);
+          o.x = fmaf(w, v.x, o.x);
+          o.y = fmaf(w, v.y, o.y);
+          o.z = fmaf(w, v.z, o.z);
+          o.w = fmaf(w, v.w, o.w);
+        };
         auto add = [&](int s0) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float w = ms[s0 + i] == m ? 1.0f : ex2_approx(ms[s0 + i] - m);
-            l = fmaf(w, ls[i], l);
-            o.x = fmaf(w, v[i].x, o.x);
-            o.y = fmaf(w, v[i].y, o.y);
-            o.z = fmaf(w, v[i].z, o.z);
-            o.w = fmaf(w, v[i].w, o.w);
-          }
+          for (int i = 0; i < 8; ++i) join(ms[s0 + i] == m ? 1.0f : ex2_approx(ms[s0 + i] - m), ls[i], v[i]);
         };
 #pragma unroll
-        for (int s = 0; s < 16; ++s)
-          ms[s] = s < 2 * splits
-                      ? ld_cluster_f32(mapa_shared(stat0 + 4u * ((s & 1) * 2 * kXTile + row), s >> 1))
-                      : -INFINITY;
+        for (int s = 0; s < 16; ++s) ms[s] = s < 2 * splits ? stat(s, 0) : -INFINITY;
         fetch(0);
 #pragma unroll
-        for (int s = 0; s < 16; ++s) m = fmaxf(m, ms[s]);
-        add(0);
-        if (splits > 4) {
-          fetch(8);
-          add(8);
+        for (int s = 0; s < 16; s += 2) m = max3_nan(m, ms[s], ms[s + 1]);
+        top = m;
+        if (__builtin_expect(m == m, 1)) {
+          add(0);
+          if (splits > 4) {
+            fetch(8);
+            add(8);
+          }
+        } else {  // a large offset among them
+          const float c = p.scale * 1.4426950408889634f;
+          top = -INFINITY;
+#pragma unroll 1
+          for (int s = 0; s < 2 * splits; ++s) top = fmaxf(top, stat(s, 2));
+#pragma unroll 1
+          for (int s = 0; s < 2 * splits; ++s) {
+            const float x = stat(s, 2);
+            join(x == top ? 1.0f : ex2_approx(xattn_ahead(x, top, c)), stat(s, 1), cols(s));
+          }
         }
-        const float f = xattn_factor(m, l);
+        const float f = xattn_factor(top, l);
         const int token = (a.row0 + row) / p.pack, head = a.h0 + (a.row0 + row) % p.pack;
         *reinterpret_cast<uint2*>(p.O + (static_cast<int64_t>(a.b) * p.Sq + token) * p.ldo + head * p.D + 4 * g) =
             make_uint2(pack_bf16x2(o.x * f, o.y * f), pack_bf16x2(o.z * f, o.w * f));
