@@ -53,6 +53,7 @@
 
 #include "attention.cuh"
 #include "sm100_warp.cuh"
+#include "xattn_ring.h"
 
 namespace w4a4 {
 
@@ -94,6 +95,7 @@ struct XAttnCfg {
   static constexpr int TILE_BYTES = DB * kXTile * 128;  // 128 rows of a head
   static constexpr int NQ = SPLIT ? 1 : 2;              // query tiles held
   static constexpr int SLOTS = (SPLIT ? 12 : 8) / DB;   // ring of key and value tiles
+  static constexpr int RINGS = SPLIT ? 2 : 1;           // one for both streams, or one each
   static constexpr int Q_OFF = 0;
   static constexpr int KV_OFF = NQ * TILE_BYTES;
   static constexpr int O_OFF = KV_OFF + SLOTS * TILE_BYTES;
@@ -107,6 +109,7 @@ struct XAttnCfg {
   static constexpr int TMEM_COLS = 512;
   static constexpr int O_COL = 256;        // S of stream t at 128 t, O at 256 + 128 t
   static_assert(SMEM <= 232448, "shared memory budget");
+  static_assert(SLOTS % RINGS == 0, "rings of equal size");
   static_assert(!SPLIT || STAT_OFF + 6 * kXTile * 4 <= O_OFF, "the partial sums fit over Q and the ring");
 };
 
@@ -297,11 +300,13 @@ __global__ void __launch_bounds__(kXThreads, 1)
     regs_release_to<kXRegsCtrl>();
     if (warp == 0 && lane == 0) {
       // ---------------------------------------------------------- keys and values
-      uint32_t fill = 0;
+      uint32_t fills[2] = {0u, 0u};
       bool ok = true;
-      auto load = [&](const CUtensorMap* map, const XTileAt& a, int j) {
-        const uint32_t s = fill % SLOTS;
-        if (!ok || !(ok = mbar_wait(smem_u32(&kv_empty[s]), ((fill / SLOTS) & 1) ^ 1, abort_flag, p.status))) return;
+      auto load = [&](const CUtensorMap* map, const XTileAt& a, int j, int ring_of) {
+        const XRing ring = xattn_ring(SLOTS, C::RINGS, ring_of);
+        uint32_t& fill = fills[ring_of];
+        const uint32_t s = ring.slot(fill);
+        if (!ok || !(ok = mbar_wait(smem_u32(&kv_empty[s]), ring.parity(fill) ^ 1, abort_flag, p.status))) return;
         const uint32_t bar = smem_u32(&kv_full[s]);
         mbar_arrive_expect_tx(bar, C::TILE_BYTES);
 #pragma unroll
@@ -314,22 +319,22 @@ __global__ void __launch_bounds__(kXThreads, 1)
         const XTileAt a = w.at(p, kRows);
         int j0, j1;
         xattn_key_range(a.len, split, splits, j0, j1);
-        if (SPLIT) {
-          // consumed in the order K0 K1 V0 K2 V1 K3 ...
-          for (int j = j0; j0 < j1 && j <= j1 && ok; ++j) {
-            if (j < j1) load(&tm_k, a, j);
-            if (j > j0) load(&tm_v, a, j - 1);
-          }
-        } else {
-          for (int j = j0; j < j1 && ok; ++j) {
-            load(&tm_k, a, j);
-            load(&tm_v, a, j);
-          }
+        for (int j = j0; j < j1 && ok; j += C::RINGS) {
+#pragma unroll
+          for (int t = 0; t < C::RINGS; ++t)
+            if (j + t < j1) load(&tm_k, a, j + t, t);
+#pragma unroll
+          for (int t = 0; t < C::RINGS; ++t)
+            if (j + t < j1) load(&tm_v, a, j + t, t);
         }
       }
       // every fill issued lands before the shared memory is released
-      for (uint32_t j = fill > SLOTS ? fill - SLOTS : 0u; j < fill; ++j)
-        mbar_wait_drain(smem_u32(&kv_full[j % SLOTS]), (j / SLOTS) & 1);
+#pragma unroll
+      for (int t = 0; t < C::RINGS; ++t) {
+        const XRing ring = xattn_ring(SLOTS, C::RINGS, t);
+        for (uint32_t j = fills[t] > ring.slots ? fills[t] - ring.slots : 0u; j < fills[t]; ++j)
+          mbar_wait_drain(smem_u32(&kv_full[ring.slot(j)]), ring.parity(j));
+      }
     } else if (warp == 3 && lane == 0) {
       // ---------------------------------------------------------- queries
       // (a thread of their own: a query tile waits for the scores of the
@@ -380,20 +385,21 @@ __global__ void __launch_bounds__(kXThreads, 1)
       auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
         return mbar_wait_warp(smem_u32(bar), parity & 1, abort_flag, p.status);
       };
-      auto slot_wait = [&](uint32_t n) -> bool { return wait(&kv_full[n % SLOTS], n / SLOTS); };
+      const XRing ring = xattn_ring(SLOTS, C::RINGS, SPLIT ? t : 0);
+      auto slot_wait = [&](uint32_t fill) -> bool { return wait(&kv_full[ring.slot(fill)], ring.parity(fill)); };
       // The two halves of a key tile have a score buffer each.  As soon as
       // the probabilities of a half are there, its product goes out and behind
       // it the next key tile's scores for the same buffer: two half tiles of
       // scores are always ahead of the softmax.
       struct Next {
         bool live;       // there is a next key tile
-        uint32_t slot;   // its keys
+        uint32_t fill;   // its keys
         bool new_q;      // it opens a work tile
         bool last;       // it closes one
       };
       uint32_t opened = 0;  // work tiles opened
       auto ready = [&](const Next& k) -> bool {
-        return (!k.new_q || wait(&q_full[SPLIT ? 0 : t], opened)) && slot_wait(k.slot);
+        return (!k.new_q || wait(&q_full[SPLIT ? 0 : t], opened)) && slot_wait(k.fill);
       };
       auto scores = [&](uint64_t kd, int h) {
 #pragma unroll
@@ -403,14 +409,15 @@ __global__ void __launch_bounds__(kXThreads, 1)
       };
       auto open = [&](const Next& k) -> bool {  // the first scores of all
         if (!ready(k)) return false;
-        const uint64_t kd = k_desc + (k.slot % SLOTS) * (C::TILE_BYTES >> 4);
+        const uint32_t k_slot = ring.slot(k.fill);
+        const uint64_t kd = k_desc + k_slot * (C::TILE_BYTES >> 4);
         tc_fence_after();
         if (elect_one()) {
           scores(kd, 0);
           tc_commit(smem_u32(&s_full[2 * t]));
           scores(kd, 1);
           tc_commit(smem_u32(&s_full[2 * t + 1]));
-          tc_commit(smem_u32(&kv_empty[k.slot % SLOTS]));
+          tc_commit(smem_u32(&kv_empty[k_slot]));
           if (k.last) tc_commit(smem_u32(&q_empty[t]));
         }
         __syncwarp();
@@ -418,13 +425,14 @@ __global__ void __launch_bounds__(kXThreads, 1)
         return true;
       };
       uint32_t it = 0, summed = 0;  // key tiles done, work tiles begun
-      auto advance = [&](uint32_t v_slot, bool fresh, const Next& k) -> bool {
-        if (!slot_wait(v_slot)) return false;
+      auto advance = [&](uint32_t v_fill, bool fresh, const Next& k) -> bool {
+        if (!slot_wait(v_fill)) return false;
         // the first product of a tile overwrites the sums of the one before
         if (!SPLIT && fresh && summed++ > 0 && !wait(&o_free[t], summed)) return false;
-        const uint64_t vd = v_desc + (v_slot % SLOTS) * (C::TILE_BYTES >> 4);
-        const uint64_t kd = k_desc + (k.slot % SLOTS) * (C::TILE_BYTES >> 4);
-        const uint32_t v_bar = smem_u32(&kv_empty[v_slot % SLOTS]), k_bar = smem_u32(&kv_empty[k.slot % SLOTS]);
+        const uint32_t v_slot = ring.slot(v_fill), k_slot = ring.slot(k.fill);
+        const uint64_t vd = v_desc + v_slot * (C::TILE_BYTES >> 4);
+        const uint64_t kd = k_desc + k_slot * (C::TILE_BYTES >> 4);
+        const uint32_t v_bar = smem_u32(&kv_empty[v_slot]), k_bar = smem_u32(&kv_empty[k_slot]);
         const uint32_t add = fresh ? 0u : 1u;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -461,11 +469,11 @@ __global__ void __launch_bounds__(kXThreads, 1)
         if (w.live(p)) {
           int j0, j1;
           xattn_key_range(w.keys(p), split, splits, j0, j1);
-          const uint32_t n = j1 - j0;
-          // the ring holds K0 K1 V0 K2 V1 K3 ..., this stream takes every second tile
-          if (static_cast<uint32_t>(t) < n && open(Next{true, static_cast<uint32_t>(t), true, false}))
-            for (uint32_t i = t; i < n; i += 2)
-              if (!advance(i + 1 < n ? 2 * i + 2 : 2 * n - 1, i < 2, Next{i + 2 < n, 2 * i + 3, false, false})) break;
+          // this stream takes every second key tile
+          const int n = (j1 - j0 + 1 - t) / 2;
+          if (n > 0 && open(Next{true, xattn_fill_k(0), true, false}))
+            for (int k = 0; k < n; ++k)
+              if (!advance(xattn_fill_v(k), k == 0, Next{k + 1 < n, xattn_fill_k(k + 1), false, false})) break;
         }
       } else {
         // the ring holds K0 V0 K1 V1 ... of the tiles with keys in turn
@@ -476,13 +484,14 @@ __global__ void __launch_bounds__(kXThreads, 1)
           return n;
         };
         int n = next_keys();
-        bool ok = n > 0 && open(Next{true, 0u, true, n == 1});
-        uint32_t slot = 1;  // the next values
+        bool ok = n > 0 && open(Next{true, xattn_fill_k(0), true, n == 1});
+        uint32_t k = 0;  // key tiles of all work tiles
         while (ok && n > 0) {
           const int n_next = next_keys();
-          for (int j = 0; ok && j < n; ++j, slot += 2) {
+          for (int j = 0; ok && j < n; ++j, ++k) {
             const bool more = j + 1 < n;
-            ok = advance(slot, j == 0, Next{more || n_next > 0, slot + 1, !more, more ? j + 2 == n : n_next == 1});
+            ok = advance(xattn_fill_v(k), j == 0,
+                         Next{more || n_next > 0, xattn_fill_k(k + 1), !more, more ? j + 2 == n : n_next == 1});
           }
           n = n_next;
         }
@@ -501,7 +510,8 @@ __global__ void __launch_bounds__(kXThreads, 1)
     const uint32_t t_s = tmem + 128 * t + lane_base, t_o = tmem + C::O_COL + 128 * t + lane_base;
     const float c = p.scale * 1.4426950408889634f;  // log2 e
     uint32_t it = 0;                // key tiles done
-    uint32_t fills = 0, closed = 0; // ring fills of the tiles before, tiles with keys done
+    uint32_t keyed = 0, closed = 0; // key tiles of the work tiles before, work tiles with keys done
+    const XRing ring = xattn_ring(SLOTS, C::RINGS, SPLIT ? t : 0);
     bool ok = true;
     auto got = [&](uint64_t* bar, uint32_t parity) -> bool {
       return mbar_wait_warp(smem_u32(bar), parity & 1, abort_flag, p.status);
@@ -550,14 +560,13 @@ __global__ void __launch_bounds__(kXThreads, 1)
           // (the second writes zeros over zeros).
           const bool clear = !((q & 1 ? keep[1] : keep[0]) >> lane & 1) && key0 + (r & 63) < p.Skv;
           if (__any_sync(0xffffffffu, clear)) {
-            const uint32_t i = u >> 1;
-            const uint32_t v = SPLIT ? (i + 1 < static_cast<uint32_t>(n) ? 2 * i + 2 : 2 * n - 1) : fills + 2 * i + 1;
-            if (!got(&kv_full[v % SLOTS], v / SLOTS)) {
+            const uint32_t fill = xattn_fill_v(SPLIT ? u >> 2 : keyed + (u >> 1));
+            if (!got(&kv_full[ring.slot(fill)], ring.parity(fill))) {
               ok = false;
               break;
             }
             if (clear) {
-              uint8_t* row = smem + C::KV_OFF + (v % SLOTS) * C::TILE_BYTES + (kXSub * h + (r & 63)) * 128 +
+              uint8_t* row = smem + C::KV_OFF + ring.slot(fill) * C::TILE_BYTES + (kXSub * h + (r & 63)) * 128 +
                              (r >> 6) * (DB == 2 ? kXTile * 128 : 64);
               // (in an order that spreads the lanes' rows over the banks)
 #pragma unroll
@@ -704,7 +713,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
         it += h;
       }
       if (!ok) break;
-      fills += 2u * n;
+      keyed += n;
       if constexpr (SPLIT) {
         // both streams' last products are done, the ring is read
         if ((some && !got(&o_done[t], 0)) || ((t == 0 ? n > 1 : n > 0) && !got(&o_done[t ^ 1], 0))) break;
