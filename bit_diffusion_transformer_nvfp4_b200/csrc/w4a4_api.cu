@@ -1351,6 +1351,7 @@ int rmsnorm_fp8(const void* X, int64_t rows, int64_t cols, int64_t ldx, const vo
   p.ldo = ldo;
   p.eps = eps;
   p.inv_cols = 1.0f / static_cast<float>(cols);
+  p.sum_min = eps >= kRowsEpsMin ? 0.0f : kRowsSumMin;
   return launch_rows_fp8<true>(p, static_cast<cudaStream_t>(stream));
 }
 

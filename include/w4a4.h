@@ -441,8 +441,9 @@ int fp8_quantize_rows(const void* X, int64_t rows, int64_t cols, int64_t ldx, ui
  *   codes, scales  out as in fp8_quantize_rows; codes NULL: neither is
  *                 written (then normed must be given)
  * Sizes and strides as in fp8_quantize_rows.  A zero row with eps 0 is NaN.
- * sum(h^2) and h * weight are fp32: where the sum overflows (|h| from about
- * 1e19) y is 0, where only the product does, infinite.
+ * sum(h^2) is taken without overflow or underflow whatever h and eps; h *
+ * weight is one fp32 product: where it overflows y is infinite, where it falls
+ * below fp32's normal range y loses low bits.
  */
 int rmsnorm_fp8(const void* X, int64_t rows, int64_t cols, int64_t ldx, const void* R, int64_t ldr,
                 const void* weight, float eps, void* hidden, int64_t ldh, void* normed, int64_t ldn,

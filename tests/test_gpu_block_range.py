@@ -128,3 +128,105 @@ def test_cross_attention_of_large_scores_under_a_mask(w4, sq):
     O = w4.cross_attention(to_dev_bf16(q), to_dev_bf16(kd), to_dev_bf16(vd), heads=2,
                            key_mask=torch.from_numpy(mask).cuda(), kv_len=torch.tensor([390], dtype=torch.int32).cuda())
     check_attention(from_dev_bf16(O), *oblock.cross_attention(q, k, v, 2, 2, 1, 1, kv_len=[390], key_mask=mask))
+
+
+# ------------------------------------------------------------------ norm
+#
+# The row factor sums up to 2^15 squares in fp32: at most 8 vectors of 8 a
+# thread, 5 + 5 additions over lanes and warps, so chains of 74; half of that
+# error after the root and six more operations: 43 x 2^-24 < 2^-18.  Scaling by
+# a power of two adds none.
+
+NORM, E4M3 = 2.0 ** -18, 2.0 ** -4
+
+
+def check_norm(w4, x, r, w, eps, in_place=None):
+    import torch
+    X = to_dev_bf16(x)
+    R = None if r is None else to_dev_bf16(r)
+    normed = torch.empty_like(X)
+    hidden = {None: None, "x": X, "r": R, "own": torch.empty_like(X)}[in_place]
+    a, hidden = w4.rms_norm_fp8(X, None if w is None else to_dev_bf16(w), residual=R, eps=eps, hidden=hidden,
+                                normed=normed)
+    _, y = oblock.rms_norm(x, r, w, np.float64(np.float32(eps)))
+    s = np.max(np.abs(y), axis=1) / 448.0
+    s = np.where(s >= 1.17549435e-38, s, 1.0)
+    got = a.scales.cpu().numpy().astype(np.float64)
+    np.testing.assert_allclose(got, s, rtol=NORM)
+    d = oblock.decode(a.codes.cpu().numpy()) * got[:, None]
+    bound = (E4M3 + 2 * NORM) * np.abs(y) + 2.0 ** -10 * got[:, None] * (1 + NORM)
+    assert np.all(np.abs(d - y) <= bound), np.max(np.abs(d - y) / bound)
+    # (half a step of a bf16 below its normal range: 2^-134)
+    np.testing.assert_allclose(from_dev_bf16(normed), y, rtol=BF16 + NORM, atol=2.0 ** -134)
+    if r is not None or in_place is not None:
+        h = x if r is None else x + r  # one fp32 addition
+        np.testing.assert_array_equal(from_dev_bf16(hidden), bf16_round(h))
+
+
+def rows_of(g, rows, cols, log2):
+    with np.errstate(under="ignore"):
+        return bf16_round((g.uniform(1.0, 2.0, (rows, cols)) * g.choice([-1.0, 1.0], (rows, cols))
+                           * 2.0 ** float(log2)).astype(np.float32))
+
+
+@pytest.mark.parametrize("cols", [8, 128, 264, 1000, 2056, 16392, 32768])
+@pytest.mark.parametrize("log2", [-130, -120, -90, -60, -50, -44, -30, 28, 45, 53, 60, 64, 90, 125])
+def test_norm_of_far_rows(w4, cols, log2):
+    """Rows whose squares leave fp32's range at either end, with and without a
+    residual, a weight, and hidden in place."""
+    g = rng(cols + 1000 + log2)
+    rows = 5 if cols > 4096 else 33
+    x, r = rows_of(g, rows, cols, log2), rows_of(g, rows, cols, log2 - 1)
+    w = bf16_round((1.0 + 0.3 * g.standard_normal(cols)).astype(np.float32))
+    w[::7] = 0.0
+    eps = 0.0 if log2 < 0 else 1e-6
+    check_norm(w4, x, None, None, eps)
+    check_norm(w4, x, None, w, eps, "own")
+    for in_place in (None, "x", "r"):
+        check_norm(w4, x, r, w, eps, in_place)
+
+
+@pytest.mark.parametrize("cols", [128, 512, 2056, 24576])
+@pytest.mark.parametrize("in_place", [None, "x", "r"])
+def test_norm_of_mixed_rows(w4, cols, in_place):
+    """Far and ordinary rows side by side, and rows that hold both kinds of
+    elements: one huge among ordinary ones, magnitudes that rise and fall
+    along the row, zeros among tiny ones."""
+    g = rng(cols + 7)
+    rows = 40 if cols < 4096 else 9
+    x, r = rows_of(g, rows, cols, 0), rows_of(g, rows, cols, -2)
+    x[1] = rows_of(g, 1, cols, 70)
+    x[2, cols // 3] = 2.0 ** 80
+    x[3] = rows_of(g, 1, cols, 0) * 2.0 ** np.linspace(-60, 100, cols).astype(np.float32).round()
+    x[4] = rows_of(g, 1, cols, 0) * 2.0 ** np.linspace(100, -60, cols).astype(np.float32).round()
+    x[5], r[5] = rows_of(g, 1, cols, -70), 0.0
+    x[6], r[6] = 0.0, 0.0
+    x[6, 5] = 2.0 ** -100
+    x[7], r[7] = rows_of(g, 1, cols, -40), 0.0
+    x[8, -1] = 2.0 ** 57
+    for eps in (1e-38, 1e-30, 1e-26, 1e-6, 1.0, 1e37):
+        check_norm(w4, x, r, None, eps, in_place)
+
+
+def test_norm_of_rows_that_are_not_numbers(w4):
+    """Zero rows with eps 0, NaN and infinities: the row NaN (the scale 1), the
+    others as they are; an infinite element NaN among zeros."""
+    import torch
+    g = rng(91)
+    for cols in (256, 4096):
+        x = rows_of(g, 12, cols, 0)
+        x[1] = 0.0
+        x[3, 17] = np.nan
+        x[5, cols - 1] = np.inf
+        x[7] = rows_of(g, 1, cols, 80)
+        X = to_dev_bf16(x)
+        X[9, 3] = float("-inf")
+        normed = torch.empty_like(X)
+        a, _ = w4.rms_norm_fp8(X, eps=0.0, normed=normed)
+        y, s, codes = from_dev_bf16(normed), a.scales.cpu().numpy(), a.codes.cpu().numpy()
+        for i in (1, 3):
+            assert np.all(np.isnan(y[i])) and s[i] == 1.0 and np.all((codes[i] & 0x7F) == 0x7F)
+        for i, j in ((5, cols - 1), (9, 3)):
+            assert np.isnan(y[i, j]) and not np.delete(y[i], j).any() and s[i] == 1.0
+        rest = [0, 2, 4, 6, 7, 8, 10, 11]
+        np.testing.assert_allclose(y[rest], oblock.rms_norm(x[rest], eps=0.0)[1], rtol=BF16 + NORM)
