@@ -267,8 +267,11 @@ def nvfp4_sf_to_rowmajor(sf_atoms, rows, K, sf_rowmajor, stream=None):
 
 def sf_rowmajor(sf_atoms: torch.Tensor, rows: int, K: int, stream=None) -> torch.Tensor:
     """The scale bytes of an SF-atom buffer as a row-major [rows, K/16] uint8 tensor."""
+    if stream is not None:
+        with _on(stream, sf_atoms.device):
+            return sf_rowmajor(sf_atoms, rows, K)
     out = torch.empty(rows, K // 16, dtype=torch.uint8, device=sf_atoms.device)
-    nvfp4_sf_to_rowmajor(sf_atoms, rows, K, out, stream)
+    nvfp4_sf_to_rowmajor(sf_atoms, rows, K, out)
     return out
 
 
@@ -291,7 +294,25 @@ def w4a4_device_status(reset: bool = False) -> int:
 
 # ------------------------------------------------------------------ tensor-level helpers
 # These allocate outputs with torch (device memory is the caller's business in
-# the C ABI) and call the raw wrappers above.
+# the C ABI) and call the raw wrappers above.  ``stream`` (a torch stream, or a
+# cudaStream_t as an integer; None: the current one) is where all of a call runs:
+# it is current while outputs and workspaces are made and while the kernels are
+# launched, as inside ``with torch.cuda.stream(stream)``.  As there, inputs must
+# be ready on it, and what another stream uses is the caller's to order.
+
+def _on(stream, device):
+    """``stream`` as the current one: memory comes from its own pool (a block
+    that another stream has just given up may still be in use there)."""
+    if device.type != "cuda":
+        raise ValueError(f"inputs on {device}, expected a CUDA device")
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = getattr(stream, "cuda_stream", stream)
+        # (cudaStreamLegacy is the default stream by another name)
+        stream = torch.cuda.ExternalStream(0 if handle == 1 else handle, device=device)
+    if stream.device != device:
+        raise ValueError(f"stream: on {stream.device}, expected {device}")
+    return torch.cuda.stream(stream)
+
 
 def _u8(n, device):
     return torch.empty(n, dtype=torch.uint8, device=device)
@@ -342,6 +363,9 @@ def quantize_act(X: torch.Tensor, inv_s=None, L1t=None, t_w=None, stream=None, a
     ``workspace``: a uint8 device tensor from ``new_workspace`` of at least
     ``nvfp4_quant_workspace_bytes(M, K, r)`` bytes, reused across calls (a
     fresh one is made when None)."""
+    if stream is not None:
+        with _on(stream, X.device):
+            return quantize_act(X, inv_s, L1t, t_w, amax=amax, workspace=workspace)
     M, K = X.shape
     r = 0 if L1t is None else int(L1t.shape[0])
     dev = X.device
@@ -351,13 +375,16 @@ def quantize_act(X: torch.Tensor, inv_s=None, L1t=None, t_w=None, stream=None, a
     U = torch.empty(M, 2 * r, dtype=torch.bfloat16, device=dev) if r else None
     ws = new_workspace(nvfp4_quant_workspace_bytes(M, K, r), dev) if workspace is None else workspace
     if amax is None:
-        nvfp4_quantize_act(X, M, K, X.stride(0), inv_s, L1t, r, t_w, Xq, Xsf, t_x, U, ws, stream)
+        nvfp4_quantize_act(X, M, K, X.stride(0), inv_s, L1t, r, t_w, Xq, Xsf, t_x, U, ws)
     else:
-        nvfp4_quantize_act_with_amax(X, M, K, X.stride(0), inv_s, L1t, r, t_w, amax, Xq, Xsf, t_x, U, ws, stream)
+        nvfp4_quantize_act_with_amax(X, M, K, X.stride(0), inv_s, L1t, r, t_w, amax, Xq, Xsf, t_x, U, ws)
     return QuantizedActivation(Xq, Xsf, t_x, U, M, K, r)
 
 
 def pack_weight(R: torch.Tensor, inv_s=None, L1t=None, L2t=None, bias=None, stream=None) -> PackedWeight:
+    if stream is not None:
+        with _on(stream, R.device):
+            return pack_weight(R, inv_s, L1t, L2t, bias)
     N, K = R.shape
     dev = R.device
     src = SRC_F32 if R.dtype == torch.float32 else SRC_BF16
@@ -365,7 +392,7 @@ def pack_weight(R: torch.Tensor, inv_s=None, L1t=None, L2t=None, bias=None, stre
     Wsf = _u8(nvfp4_sf_bytes(N, K), dev)
     t_w = torch.empty(1, dtype=torch.float32, device=dev)
     ws = new_workspace(nvfp4_quant_workspace_bytes(N, K, 0), dev)
-    nvfp4_pack_weight(R, src, N, K, R.stride(0), Wq, Wsf, t_w, ws, stream)
+    nvfp4_pack_weight(R, src, N, K, R.stride(0), Wq, Wsf, t_w, ws)
     return PackedWeight(Wq, Wsf, t_w, N, K, inv_s, L1t, L2t, bias)
 
 
@@ -374,14 +401,17 @@ def gemm(qa: QuantizedActivation, w: PackedWeight, epilogue: int = EPI_NONE, Y=N
     """Y = the fused W4A4 GEMM.  With ``next_amax`` (fp32 device scalar holding
     a non-negative value, normally 0) it also max-es in the tensor amax
     max |fl(Y * next_inv_s)| that the next layer's quantiser needs."""
+    if stream is not None:
+        with _on(stream, qa.Xq.device):
+            return gemm(qa, w, epilogue, Y, next_inv_s=next_inv_s, next_amax=next_amax)
     if Y is None:
         Y = torch.empty(qa.M, w.N, dtype=torch.bfloat16, device=qa.Xq.device)
     if next_amax is None:
         w4a4_gemm(qa.Xq, qa.Xsf, qa.t_x, qa.U, qa.M, w.N, w.K, w.Wq, w.Wsf, w.t_w, w.L2t, w.r, w.bias,
-                  epilogue, Y, Y.stride(0), stream)
+                  epilogue, Y, Y.stride(0))
     else:
         w4a4_gemm_next_amax(qa.Xq, qa.Xsf, qa.t_x, qa.U, qa.M, w.N, w.K, w.Wq, w.Wsf, w.t_w, w.L2t, w.r, w.bias,
-                            epilogue, Y, Y.stride(0), next_inv_s, next_amax, stream)
+                            epilogue, Y, Y.stride(0), next_inv_s, next_amax)
     return Y
 
 
@@ -391,6 +421,9 @@ def gemm_swiglu(qa: QuantizedActivation, w: PackedWeight, n_plain: int, Y=None, 
     packed weight rows give Y [M, n_plain]; the rest, gate/up pairs in the
     order of ``prep.swiglu_row_order``, give H = silu(gate) * up [M, (N -
     n_plain) / 2].  Returns (Y, H)."""
+    if stream is not None:
+        with _on(stream, qa.Xq.device):
+            return gemm_swiglu(qa, w, n_plain, Y, H, next_inv_s=next_inv_s, next_amax=next_amax)
     n_h = (w.N - n_plain) // 2
     dev = qa.Xq.device
     if Y is None and n_plain > 0:
@@ -398,7 +431,7 @@ def gemm_swiglu(qa: QuantizedActivation, w: PackedWeight, n_plain: int, Y=None, 
     if H is None:
         H = torch.empty(qa.M, n_h, dtype=torch.bfloat16, device=dev)
     w4a4_gemm_swiglu(qa.Xq, qa.Xsf, qa.t_x, qa.U, qa.M, w.N, w.K, w.Wq, w.Wsf, w.t_w, w.L2t, w.r, w.bias, n_plain,
-                     Y, Y.stride(0) if Y is not None else 0, H, H.stride(0), next_inv_s, next_amax, stream)
+                     Y, Y.stride(0) if Y is not None else 0, H, H.stride(0), next_inv_s, next_amax)
     return Y, H
 
 
@@ -409,6 +442,9 @@ def gemm_rope(qa: QuantizedActivation, w: PackedWeight, rope, n_rope: int, d_hea
     token the (cos, sin) of each feature pair, interleaved) and, with
     ``n_plain`` < N, the SwiGLU epilogue on the rest as in ``gemm_swiglu``.
     Returns (Y, H); H is None without SwiGLU outputs."""
+    if stream is not None:
+        with _on(stream, qa.Xq.device):
+            return gemm_rope(qa, w, rope, n_rope, d_head, n_plain, Y, H, next_inv_s=next_inv_s, next_amax=next_amax)
     dev = qa.Xq.device
     n_plain = w.N if n_plain is None else n_plain
     if Y is None:
@@ -417,7 +453,7 @@ def gemm_rope(qa: QuantizedActivation, w: PackedWeight, rope, n_rope: int, d_hea
         H = torch.empty(qa.M, (w.N - n_plain) // 2, dtype=torch.bfloat16, device=dev)
     w4a4_gemm_rope(qa.Xq, qa.Xsf, qa.t_x, qa.U, qa.M, w.N, w.K, w.Wq, w.Wsf, w.t_w, w.L2t, w.r, w.bias, n_rope,
                    d_head, rope, rope.stride(0), n_plain, Y, Y.stride(0), H, 0 if H is None else H.stride(0),
-                   next_inv_s, next_amax, stream)
+                   next_inv_s, next_amax)
     return Y, H
 
 
@@ -432,6 +468,9 @@ class Fp8Tensor:
 def quantize_fp8(X, transpose: bool = False, out=None, workspace=None, stream=None) -> Fp8Tensor:
     """Per-tensor E4M3 quantisation of a bf16 [rows, cols] view (row stride
     X.stride(0)); transposed codes [cols, rows] with ``transpose``."""
+    if stream is not None:
+        with _on(stream, X.device):
+            return quantize_fp8(X, transpose, out, workspace)
     rows, cols = X.shape
     dev = X.device
     if out is None:
@@ -439,7 +478,7 @@ def quantize_fp8(X, transpose: bool = False, out=None, workspace=None, stream=No
     scale = torch.empty(1, dtype=torch.float32, device=dev)
     if workspace is None:
         workspace = torch.empty(max(fp8_quant_workspace_bytes(rows, cols), 16), dtype=torch.uint8, device=dev)
-    fp8_quantize(X, rows, cols, X.stride(0), transpose, out, out.stride(0), scale, workspace, stream)
+    fp8_quantize(X, rows, cols, X.stride(0), transpose, out, out.stride(0), scale, workspace)
     return Fp8Tensor(out, scale, rows, cols, transpose)
 
 
@@ -448,12 +487,15 @@ def attention(q: Fp8Tensor, k: Fp8Tensor, vt: Fp8Tensor, heads: int, batch: int 
     """FP8 attention over ``batch`` sequences of q.rows / batch tokens, heads
     of 128 features; q, k row-major codes [tokens, heads*128], vt the values'
     transposed codes [heads*128, tokens].  Returns bf16 O [tokens, heads*128]."""
+    if stream is not None:
+        with _on(stream, q.codes.device):
+            return attention(q, k, vt, heads, batch, O, softmax_scale)
     S = q.rows // batch
     if O is None:
         O = torch.empty(q.rows, heads * 128, dtype=torch.bfloat16, device=q.codes.device)
     c = 1.0 / math.sqrt(128.0) if softmax_scale is None else softmax_scale
     attention_fp8(q.codes, k.codes, vt.codes, batch, S, heads, q.codes.stride(0), k.codes.stride(0),
-                  vt.codes.stride(0), q.scale, k.scale, vt.scale, c, O, O.stride(0), stream)
+                  vt.codes.stride(0), q.scale, k.scale, vt.scale, c, O, O.stride(0))
     return O
 
 
@@ -481,13 +523,10 @@ def _vector(name, t, dtype, dev, n):
                          f"strides {t.stride()} on {t.device}")
 
 
-def _launch(fn, dev, stream, *args):
+def _launch(fn, dev, *args):
     """Calls an entry point with ``dev`` current (the library works on the
-    current device) on the given stream or ``dev``'s current one."""
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(dev)
-    else:
-        stream = getattr(stream, "cuda_stream", stream)
+    current device) on ``dev``'s current stream."""
+    stream = torch._C._cuda_getCurrentRawStream(dev)
     call = getattr(_lib or lib(), fn)
     if torch._C._cuda_getDevice() == dev:
         status = call(*args, stream)
@@ -540,11 +579,14 @@ def _row_outputs(rows, cols, dev, device, codes, scales):
 def quantize_rows_fp8(X, codes=None, scales=None, stream=None) -> Fp8Rows:
     """E4M3 codes of a bf16 [rows, cols] view, one scale per row (cols a
     multiple of 8, at most MAX_ROW_COLS)."""
+    if stream is not None:
+        with _on(stream, X.device):
+            return quantize_rows_fp8(X, codes, scales)
     dev = X.get_device()
     ldx = _matrix("X", X, torch.bfloat16, dev)
     rows, cols = X.shape
     codes, ldo, scales = _row_outputs(rows, cols, dev, X.device, codes, scales)
-    _launch("fp8_quantize_rows", dev, stream, X.data_ptr(), rows, cols, ldx, codes.data_ptr(), ldo, scales.data_ptr())
+    _launch("fp8_quantize_rows", dev, X.data_ptr(), rows, cols, ldx, codes.data_ptr(), ldo, scales.data_ptr())
     return Fp8Rows(codes, scales)
 
 
@@ -556,6 +598,9 @@ def rms_norm_fp8(X, weight=None, residual=None, eps=1e-6, hidden=None, normed=No
     (in place with ``hidden=X`` or ``hidden=residual``), else None unless a
     tensor is passed.  ``normed``: a bf16 tensor that also receives the norm
     itself, for a W4A4 layer behind it (``quantize_act``)."""
+    if stream is not None:
+        with _on(stream, X.device):
+            return rms_norm_fp8(X, weight, residual, eps, hidden, normed, codes, scales)
     dev = X.get_device()
     ldx = _matrix("X", X, torch.bfloat16, dev)
     rows, cols = X.shape
@@ -577,7 +622,7 @@ def rms_norm_fp8(X, weight=None, residual=None, eps=1e-6, hidden=None, normed=No
         _vector("weight", weight, torch.bfloat16, dev, cols)
         w = weight.data_ptr()
     codes, ldo, scales = _row_outputs(rows, cols, dev, X.device, codes, scales)
-    _launch("rmsnorm_fp8", dev, stream, X.data_ptr(), rows, cols, ldx, r, ldr, w, eps, h, ldh, n, ldn,
+    _launch("rmsnorm_fp8", dev, X.data_ptr(), rows, cols, ldx, r, ldr, w, eps, h, ldh, n, ldn,
             codes.data_ptr(), ldo, scales.data_ptr())
     return Fp8Rows(codes, scales), hidden
 
@@ -592,6 +637,9 @@ def linear_fp8(a, w: PackedWeightFp8, activation: int = EPI_NONE, residual=None,
     """Y = activation(a w^T + bias) + residual in bf16 [rows, N], on E4M3
     codes: ``a`` an Fp8Rows (a scale per row) or a row-major Fp8Tensor (one
     scale).  ``Y`` may be ``residual`` itself."""
+    if stream is not None:
+        with _on(stream, a.codes.device):
+            return linear_fp8(a, w, activation, residual, Y)
     per_row = isinstance(a, Fp8Rows)
     if not per_row and a.transposed:
         raise ValueError("a: row-major codes expected")
@@ -614,7 +662,7 @@ def linear_fp8(a, w: PackedWeightFp8, activation: int = EPI_NONE, residual=None,
         Y, ldy = torch.empty(M, N, dtype=torch.bfloat16, device=codes.device), N
     else:
         ldy = _matrix("Y", Y, torch.bfloat16, dev, M, N)
-    _launch("fp8_gemm", dev, stream, codes.data_ptr(), lda, s_a.data_ptr(), int(per_row), M, N, K, w.codes.data_ptr(),
+    _launch("fp8_gemm", dev, codes.data_ptr(), lda, s_a.data_ptr(), int(per_row), M, N, K, w.codes.data_ptr(),
             ldw, w.scales.data_ptr(), b, activation, r, ldr, Y.data_ptr(), ldy)
     return Y
 
@@ -628,6 +676,9 @@ def cross_attention(q, k, v, heads: int, kv_heads=None, batch: int = 1, kv_batch
     int32 [kv_batch], the keys that count; ``key_mask``: bool or uint8
     [kv_batch, Skv], False for keys that do not.  Returns bf16 O
     [batch*Sq, heads*d]; a query without keys gets 0."""
+    if stream is not None:
+        with _on(stream, q.device):
+            return cross_attention(q, k, v, heads, kv_heads, batch, kv_batch, kv_len, key_mask, O, softmax_scale)
     kv_heads = heads if kv_heads is None else kv_heads
     kv_batch = batch if kv_batch is None else kv_batch
     dev = q.get_device()
@@ -656,7 +707,7 @@ def cross_attention(q, k, v, heads: int, kv_heads=None, batch: int = 1, kv_batch
     else:
         ldo = _matrix("O", O, torch.bfloat16, dev, rows, width)
     c = 1.0 / math.sqrt(d) if softmax_scale is None else softmax_scale
-    _launch("cross_attention_bf16", dev, stream, q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, batch,
+    _launch("cross_attention_bf16", dev, q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, batch,
             kv_batch, rows // batch, Skv, heads, kv_heads, d, n, m, ldm, c, O.data_ptr(), ldo)
     return O
 
@@ -668,6 +719,10 @@ def gemm_quantize_next(qa: QuantizedActivation, w: PackedWeight, next_t, next_in
     scale bytes of its final outputs (Y, or H with ``n_plain`` < N) under
     the given tensor scale ``next_t``.  Returns (Y, H, next_q, next_sf);
     Y / H are None when not stored."""
+    if stream is not None:
+        with _on(stream, qa.Xq.device):
+            return gemm_quantize_next(qa, w, next_t, next_inv_s, epilogue, n_plain, store_outputs, next_K, next_col,
+                                      next_q, next_sf, next_amax)
     dev = qa.Xq.device
     n_plain = w.N if n_plain is None else n_plain
     n_out = w.N if n_plain == w.N else (w.N - n_plain) // 2
@@ -687,17 +742,19 @@ def gemm_quantize_next(qa: QuantizedActivation, w: PackedWeight, next_t, next_in
         next_sf = torch.zeros(nvfp4_sf_bytes(qa.M, next_K), dtype=torch.uint8, device=dev)
     w4a4_gemm_quantize_next(qa.Xq, qa.Xsf, qa.t_x, qa.U, qa.M, w.N, w.K, w.Wq, w.Wsf, w.t_w, w.L2t, w.r, w.bias,
                             epilogue, n_plain, Y, 0 if Y is None else Y.stride(0), H, 0 if H is None else H.stride(0),
-                            next_inv_s, next_t, next_q, next_q.stride(0), next_sf, next_K, next_col, next_amax,
-                            stream)
+                            next_inv_s, next_t, next_q, next_q.stride(0), next_sf, next_K, next_col, next_amax)
     return Y, H, next_q, next_sf
 
 
 def linear(X: torch.Tensor, w: PackedWeight, epilogue: int = EPI_NONE, Y=None, workspace=None, stream=None):
+    if stream is not None:
+        with _on(stream, X.device):
+            return linear(X, w, epilogue, Y, workspace)
     M, K = X.shape
     if Y is None:
         Y = torch.empty(M, w.N, dtype=torch.bfloat16, device=X.device)
     if workspace is None:
         workspace = new_workspace(w4a4_workspace_bytes(M, w.N, K, w.r), X.device)
     w4a4_linear(X, M, w.N, K, w.Wq, w.Wsf, w.t_w, w.inv_s, w.L1t, w.L2t, w.r, w.bias, epilogue, Y,
-                workspace, stream)
+                workspace)
     return Y
