@@ -37,6 +37,9 @@ struct DeviceInfo {
   bool ok = false;
   int num_sms = 0;
   int* status_ptr = nullptr;
+  // set-up of the layers between the W4A4 ones, each at its own first call: 0 not
+  // done, else 1 + whether it worked
+  int fp8_gemm_set = 0, xattn_set = 0;
   int xattn_clusters[9] = {};  // clusters of 1 .. 8 of the split cross attention that are resident at once
 };
 DeviceInfo g_dev[kMaxDevices];
@@ -136,43 +139,68 @@ int device_setup(DeviceInfo** out) {
   attr_ok &= cudaFuncSetAttribute(gemm2_kernel<PairRope>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   PairRope::SMEM) == cudaSuccess;
 
-  attr_ok &= smem_attr<Fp8Pair256>(gemm_fp8_pair_kernel<Fp8Pair256>) &&
-             smem_attr<Fp8Pair128>(gemm_fp8_pair_kernel<Fp8Pair128>) &&
-             smem_attr<Fp8Pair64>(gemm_fp8_pair_kernel<Fp8Pair64>);
-  attr_ok &= smem_attr<Fp8Small16>(gemm_fp8_small_kernel<Fp8Small16>) &&
-             smem_attr<Fp8Small32>(gemm_fp8_small_kernel<Fp8Small32>) &&
-             smem_attr<Fp8Small64>(gemm_fp8_small_kernel<Fp8Small64>) &&
-             smem_attr<Fp8Small128>(gemm_fp8_small_kernel<Fp8Small128>);
-  attr_ok &= smem_attr<XAttnCfg<1, false>>(cross_attention_kernel<XAttnCfg<1, false>>) &&
-             smem_attr<XAttnCfg<2, false>>(cross_attention_kernel<XAttnCfg<2, false>>) &&
-             smem_attr<XAttnCfg<1, true>>(cross_attention_kernel<XAttnCfg<1, true>>) &&
-             smem_attr<XAttnCfg<2, true>>(cross_attention_kernel<XAttnCfg<2, true>>);
-
-  // (one CTA per SM; clusters stay within a GPC, so larger ones leave SMs over)
-  for (int c = 1; c <= 8; ++c) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(c), static_cast<unsigned>(d.num_sms), 1);
-    cfg.blockDim = dim3(kXThreads, 1, 1);
-    cfg.dynamicSmemBytes = XAttnCfg<2, true>::SMEM;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(c);
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, cross_attention_kernel<XAttnCfg<2, true>>, &cfg) != cudaSuccess || n < 1) {
-      cudaGetLastError();
-      n = std::max(d.num_sms / c, 1);  // (only a cost: the launch is valid either way)
-    }
-    d.xattn_clusters[c] = n;
-  }
-
   if (!attr_ok) { cudaGetLastError(); return W4A4_ERR_CUDA; }
   d.ok = true;
   *out = &d;
   return W4A4_OK;
+}
+
+// The same for the FP8 linear layer and for the cross attention, which calls of
+// the others do not wait for and whose failure is not theirs.
+int fp8_gemm_setup(DeviceInfo** out) {
+  const int st = device_setup(out);
+  if (st != W4A4_OK) return st;
+  std::lock_guard<std::mutex> lock(g_mu);
+  DeviceInfo& d = **out;
+  if (d.fp8_gemm_set == 0) {
+    const bool ok = smem_attr<Fp8Pair256>(gemm_fp8_pair_kernel<Fp8Pair256>) &&
+                    smem_attr<Fp8Pair128>(gemm_fp8_pair_kernel<Fp8Pair128>) &&
+                    smem_attr<Fp8Pair64>(gemm_fp8_pair_kernel<Fp8Pair64>) &&
+                    smem_attr<Fp8Small16>(gemm_fp8_small_kernel<Fp8Small16>) &&
+                    smem_attr<Fp8Small32>(gemm_fp8_small_kernel<Fp8Small32>) &&
+                    smem_attr<Fp8Small64>(gemm_fp8_small_kernel<Fp8Small64>) &&
+                    smem_attr<Fp8Small128>(gemm_fp8_small_kernel<Fp8Small128>);
+    if (!ok) cudaGetLastError();
+    d.fp8_gemm_set = ok ? 2 : 1;
+  }
+  return d.fp8_gemm_set == 2 ? W4A4_OK : W4A4_ERR_CUDA;
+}
+
+int xattn_setup(DeviceInfo** out) {
+  const int st = device_setup(out);
+  if (st != W4A4_OK) return st;
+  std::lock_guard<std::mutex> lock(g_mu);
+  DeviceInfo& d = **out;
+  if (d.xattn_set == 0) {
+    const bool ok = smem_attr<XAttnCfg<1, false>>(cross_attention_kernel<XAttnCfg<1, false>>) &&
+                    smem_attr<XAttnCfg<2, false>>(cross_attention_kernel<XAttnCfg<2, false>>) &&
+                    smem_attr<XAttnCfg<1, true>>(cross_attention_kernel<XAttnCfg<1, true>>) &&
+                    smem_attr<XAttnCfg<2, true>>(cross_attention_kernel<XAttnCfg<2, true>>);
+    if (!ok) cudaGetLastError();
+    // (one CTA per SM; clusters stay within a GPC, so larger ones leave SMs over)
+    for (int c = 1; ok && c <= 8; ++c) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(static_cast<unsigned>(c), static_cast<unsigned>(d.num_sms), 1);
+      cfg.blockDim = dim3(kXThreads, 1, 1);
+      cfg.dynamicSmemBytes = XAttnCfg<2, true>::SMEM;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = static_cast<unsigned>(c);
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      int n = 0;
+      if (cudaOccupancyMaxActiveClusters(&n, cross_attention_kernel<XAttnCfg<2, true>>, &cfg) != cudaSuccess ||
+          n < 1) {
+        cudaGetLastError();
+        n = std::max(d.num_sms / c, 1);  // (only a cost: the launch is valid either way)
+      }
+      d.xattn_clusters[c] = n;
+    }
+    d.xattn_set = ok ? 2 : 1;
+  }
+  return d.xattn_set == 2 ? W4A4_OK : W4A4_ERR_CUDA;
 }
 
 bool encode_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* ptr, uint64_t inner, uint64_t outer,
@@ -1372,7 +1400,7 @@ int fp8_gemm(const uint8_t* A8, int64_t lda, const float* s_a, int s_a_rows, int
       reinterpret_cast<uintptr_t>(s_a) % 4 != 0)
     return W4A4_ERR_ALIGN;
   DeviceInfo* dev = nullptr;
-  int st = device_setup(&dev);
+  int st = fp8_gemm_setup(&dev);
   if (st != W4A4_OK) return st;
   Fp8GemmParams p = {};
   p.M = static_cast<int>(M);
@@ -1424,7 +1452,7 @@ int cross_attention_bf16(const void* Q, int64_t ldq, const void* K, int64_t ldk,
   if (!aligned16(Q) || !aligned16(K) || !aligned16(V) || !aligned16(O) || reinterpret_cast<uintptr_t>(kv_len) % 4 != 0)
     return W4A4_ERR_ALIGN;
   DeviceInfo* dev = nullptr;
-  int st = device_setup(&dev);
+  int st = xattn_setup(&dev);
   if (st != W4A4_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (Skv == 0) {  // no keys: every row is 0
