@@ -19,7 +19,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libw4a4.so")
 SOURCES = ["w4a4_api.cu"]
 DEPS = ["w4a4_api.cu", "attention.cuh", "cross_attention.cuh", "gemm.cuh", "gemm2.cuh", "gemm_fp8.cuh", "mma_rate.cuh",
-        "quant.cuh", "rows_fp8.cuh", "sm100.cuh", "sm100_warp.cuh", "xattn_ring.h"]
+        "plan.h", "quant.cuh", "rows_fp8.cuh", "sm100.cuh", "sm100_warp.cuh", "xattn_ring.h"]
 
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]
 

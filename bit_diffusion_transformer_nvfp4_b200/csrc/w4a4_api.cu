@@ -21,6 +21,7 @@
 #include "cross_attention.cuh"
 #include "gemm_fp8.cuh"
 #include "mma_rate.cuh"
+#include "plan.h"
 #include "rows_fp8.cuh"
 
 namespace w4a4 {
@@ -67,7 +68,6 @@ using Fp8Small64 = Fp8SmallCfg<64, 4>;
 using Fp8Small128 = Fp8SmallCfg<128, 3>;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t round256(size_t v) { return (v + 255) & ~size_t(255); }
 
 template <class C, class Kernel>
@@ -801,51 +801,6 @@ int launch_fp8_pair(const uint8_t* A8, int64_t lda, const uint8_t* W8, int64_t l
   return W4A4_OK;
 }
 
-// K slices of the kernel for few rows: a power of two up to a cluster of
-// eight, at most one per 128-deep step, while the CTAs still fit on the device
-// at once: two per SM, but clusters of four and eight do not pack that densely
-// (9216 x 3200 at one token: 144 CTAs in pairs 8.2 us, 288 in fours 12.2 us;
-// 6144 x 6144: 192 in fours 11.2 us, 96 in pairs 11.7 us).
-int fp8_small_splits(int64_t n_tiles, int64_t k_steps, int64_t sms) {
-  int s = 1;
-  while (s < 8 && 2 * s <= k_steps && n_tiles * 2 * s <= (s == 1 ? 2 * sms : sms + sms / 2)) s *= 2;
-  return s;
-}
-
-// Which FP8 kernel a product takes, by its time on one B200 in units of 10 ns,
-// fitted to products of 24 to 9216 rows, 280 to 18432 columns and K from 512
-// to 8192 (most within 10 %).  Pairs: a beginning and end, and waves of tiles,
-// each of its K steps or, where K is short, of the tile's epilogue.  Few rows:
-// the K steps of a slice, dearer with more tokens a tile and with more than
-// one CTA on an SM, and the exchange of the partial sums.
-// Measured on both sides: 64 x 18432 x 6144 25.7 us by the weight, 27.5 by
-// pairs, 100 x 9216 x 3200 13.3 and 10.6; 333 x 2056 x 4112 13.4, 15.4 and 18.8
-// with tiles 64, 128 and 256 wide, 9216 x 640 x 512 11.3, 10.3 and 10.3, 640 x
-// 6144 x 6144 40.8, 27.7 and 25.0, 1729 x 4528 x 1536 23.0, 18.5 and 14.5.
-// Returns 0 for the kernel for few rows, else the tile width.
-int fp8_gemm_plan(int64_t M, int64_t N, int64_t K, int64_t sms) {
-  const int64_t k_steps = ceil_div(K, 128), n_tiles = ceil_div(N, 128);
-  int best = 256;
-  int64_t cost = INT64_MAX;
-  const int width[3] = {64, 128, 256}, ends[3] = {508, 498, 542}, step[3] = {19, 24, 37}, epilogue[3] = {131, 210, 343};
-  for (int i = 0; i < 3; ++i) {
-    const int64_t waves = ceil_div(ceil_div(M, 256) * ceil_div(N, width[i]), sms / 2);
-    const int64_t c = ends[i] + waves * std::max<int64_t>(k_steps * step[i], epilogue[i]);
-    if (c < cost) {
-      cost = c;
-      best = width[i];
-    }
-  }
-  if (M <= 128 && n_tiles <= 65535) {
-    const int64_t ctas = n_tiles * fp8_small_splits(n_tiles, k_steps, sms);
-    const int64_t steps = ceil_div(k_steps * n_tiles, ctas);
-    const int64_t c = 500 + 460 * M / 128 + steps * (19 + 11 * M / 128) * std::max(ctas, sms) / sms +
-                      910 * M / 128 * std::max<int64_t>(ctas - sms, 0) / sms;
-    if (M <= 16 || c < cost) best = 0;
-  }
-  return best;
-}
-
 template <class C>
 int launch_fp8_small(const uint8_t* A8, int64_t lda, const uint8_t* W8, int64_t ldw, const Fp8GemmParams& p,
                      cudaStream_t stream, DeviceInfo* dev) {
@@ -893,29 +848,6 @@ bool encode_heads(CUtensorMap* m, const void* ptr, int64_t D, int64_t heads, int
   return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Which form a problem takes: 0 the persistent one (256 rows a work tile), else
-// the split one (128 rows) with that many CTAs of a cluster on the keys of a
-// tile, by their time on one B200 in units of 0.1 us.  Persistent: 1.7 us a
-// key tile and 3 us a work tile, one after the other on an SM.  Split: 7 us
-// and 1.4 us a key tile, in waves of the clusters that are resident at once
-// (B200: 74 of two, 33 of four, 15 of eight).
-// Measured: 4 x 1 query, 4109 keys, 32 heads on 8: 17.5 us in fours; 1 query,
-// 4096 keys, 16 heads: 12.8 us in one wave of clusters, 21.5 in two of eights.
-int xattn_splits(int64_t rows, int64_t head_blocks, int64_t key_tiles, const DeviceInfo& dev) {
-  int best = 0;
-  int64_t cost = ceil_div(ceil_div(rows, 2 * kXTile) * head_blocks, dev.num_sms) * (17 * key_tiles + 30) + 30;
-  const int64_t units = ceil_div(rows, kXTile) * head_blocks;
-  if (units > 65535) return best;
-  for (int s = 1; s <= 8 && s <= key_tiles; ++s) {
-    const int64_t c = ceil_div(units, dev.xattn_clusters[s]) * (14 * ceil_div(key_tiles, s) + 70);
-    if (c < cost) {
-      cost = c;
-      best = s;
-    }
-  }
-  return best;
 }
 
 template <class C>
@@ -1481,7 +1413,8 @@ int cross_attention_bf16(const void* Q, int64_t ldq, const void* K, int64_t ldk,
   p.O = static_cast<__nv_bfloat16*>(O);
   p.ldo = ldo;
   p.status = dev->status_ptr;
-  const int splits = xattn_splits(Sq * p.pack, batch * (heads / p.pack), ceil_div(Skv, kXTile), *dev);
+  const int splits = xattn_splits(Sq * p.pack, batch * (heads / p.pack), ceil_div(Skv, kXTile), dev->num_sms,
+                                  dev->xattn_clusters);
   if (splits > 0)
     return d_head <= 64 ? launch_cross_attention<XAttnCfg<1, true>>(Q, ldq, K, ldk, V, ldv, p, splits, s, dev)
                         : launch_cross_attention<XAttnCfg<2, true>>(Q, ldq, K, ldk, V, ldv, p, splits, s, dev);

@@ -1,0 +1,74 @@
+"""GPU parity of every kernel of the FP8 linear layer, at sizes that are known
+(on the CPU) to reach them, against 64-bit references.
+
+Linear: the codes are 0, +-0.5, +-1 and +-2, so every partial sum is exact in
+fp32 on the GPU and in the reference (products of whole numbers up to 16, sums
+below 2^24); what is left is four fp32 operations, the hardware exponential of
+the GELU (2^-20 of its argument's terms) and the output's bf16 rounding, 2^-8.
+"""
+import math
+
+import numpy as np
+import pytest
+
+from helpers import from_dev_bf16, to_dev_bf16, to_dev_f32
+from oracle import block as oblock
+from plan_shapes import PRODUCTS
+from synth import bf16_round, rng
+
+pytestmark = pytest.mark.gpu
+
+BF16 = 2.0 ** -8
+CODES = np.array([0x00, 0x30, 0x38, 0x40, 0xB0, 0xB8, 0xC0], np.uint8)  # 0, +-0.5, +-1, +-2
+
+
+@pytest.fixture(scope="module")
+def w4():
+    import torch
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    import bit_diffusion_transformer_nvfp4_b200 as w
+    w.lib()
+    return w
+
+
+@pytest.fixture(autouse=True)
+def clean_status(w4):
+    import torch
+    yield
+    torch.cuda.synchronize()
+    assert w4.w4a4_device_status() == 0
+
+
+def doubled(codes):
+    """Twice the codes' values, whole numbers, in fp32."""
+    return (2 * oblock.decode(codes)).astype(np.float32)
+
+
+@pytest.mark.parametrize("M,N,K", [p[:3] for p in PRODUCTS])
+def test_linear_of_every_kernel(w4, M, N, K):
+    """All four of GELU or none, with and without residual, in turn with and
+    without bias; rows and columns behind the output stay."""
+    import torch
+    g = rng(M * 5 + N + K)
+    a, w = CODES[g.integers(0, 7, (M, K))], CODES[g.integers(0, 7, (N, K))]
+    s_a = np.exp(0.5 * g.standard_normal(M)).astype(np.float32)
+    s_w = (np.exp(0.5 * g.standard_normal(N)) / math.sqrt(K)).astype(np.float32)
+    b = bf16_round(g.standard_normal(N).astype(np.float32))
+    r = bf16_round(g.standard_normal((M, N)).astype(np.float32))
+    t = (doubled(a) @ doubled(w).T).astype(np.float64) / 4 * s_a[:, None].astype(np.float64) * s_w[None, :]
+    A = w4.Fp8Rows(torch.from_numpy(a).cuda(), to_dev_f32(s_a))
+    codes, scales, B, R = torch.from_numpy(w).cuda(), to_dev_f32(s_w), to_dev_bf16(b), to_dev_bf16(r)
+    for gelu, residual, bias in ((False, False, True), (True, False, False), (False, True, False), (True, True, True)):
+        want = t + b if bias else t.copy()
+        size = np.abs(t) + (np.abs(b) if bias else 0.0) + (np.abs(r) if residual else 0.0)
+        if gelu:
+            want = oblock.gelu_tanh(want)
+        if residual:
+            want = want + r
+        base = torch.full((M + 1, N + 8), 3.0, dtype=torch.bfloat16, device="cuda")
+        w4.linear_fp8(A, w4.PackedWeightFp8(codes, scales, B if bias else None), residual=R if residual else None,
+                      activation=w4.EPI_GELU_TANH if gelu else w4.EPI_NONE, Y=base[:M, :N])
+        err = np.abs(from_dev_bf16(base[:M, :N].contiguous()) - want)
+        bound = BF16 * np.abs(want) + 2.0 ** -19 * size + 2.0 ** -133
+        assert np.all(err <= bound), (gelu, residual, np.max(err / bound))
+        assert bool((base[M:] == 3.0).all()) and bool((base[:, N:] == 3.0).all())
