@@ -1,10 +1,13 @@
-"""GPU parity of every kernel of the FP8 linear layer, at sizes that are known
-(on the CPU) to reach them, against 64-bit references.
+"""GPU parity of every kernel of the FP8 linear layer and both forms of the
+cross attention, at sizes that are known (on the CPU) to reach them, against
+64-bit references.
 
 Linear: the codes are 0, +-0.5, +-1 and +-2, so every partial sum is exact in
 fp32 on the GPU and in the reference (products of whole numbers up to 16, sums
 below 2^24); what is left is four fp32 operations, the hardware exponential of
 the GELU (2^-20 of its argument's terms) and the output's bf16 rounding, 2^-8.
+Attention: as for the ordinary cases (weights rounded to bf16, 2^-8, an
+exponential good to 2^-13, the output's own 2^-8).
 """
 import math
 
@@ -13,7 +16,7 @@ import pytest
 
 from helpers import from_dev_bf16, to_dev_bf16, to_dev_f32
 from oracle import block as oblock
-from plan_shapes import PRODUCTS
+from plan_shapes import ATTENTION, PRODUCTS
 from synth import bf16_round, rng
 
 pytestmark = pytest.mark.gpu
@@ -72,3 +75,32 @@ def test_linear_of_every_kernel(w4, M, N, K):
         bound = BF16 * np.abs(want) + 2.0 ** -19 * size + 2.0 ** -133
         assert np.all(err <= bound), (gelu, residual, np.max(err / bound))
         assert bool((base[M:] == 3.0).all()) and bool((base[:, N:] == 3.0).all())
+
+
+@pytest.mark.parametrize("batch,kv_batch,sq,sk,heads,kv_heads,d", [a[:7] for a in ATTENTION])
+@pytest.mark.parametrize("what", ["all", "length", "mask", "both", "none"])
+def test_cross_attention_of_shared_states(w4, batch, kv_batch, sq, sk, heads, kv_heads, d, what):
+    """Every sequence attends to the same keys, under one length and one mask."""
+    import torch
+    g = rng(sq + sk + d)
+    q = bf16_round((1.5 * g.standard_normal((batch * sq, heads * d))).astype(np.float32))
+    k, v = (bf16_round(g.standard_normal((kv_batch * sk, kv_heads * d)).astype(np.float32)) for _ in range(2))
+    n = np.array([sk - 77], np.int32) if what in ("length", "both") else None
+    if what == "none":
+        n = np.array([0], np.int32)
+    mask = g.random((1, sk)) < 0.6 if what in ("mask", "both") else None
+    kd, vd = k.copy(), v.copy()
+    gone = np.zeros(sk, bool)
+    if n is not None:
+        gone |= np.arange(sk) >= n[0]
+    if mask is not None:
+        mask[0, 128:256] = False
+        gone |= ~mask[0]
+    kd[gone], vd[gone] = np.nan, np.inf
+    O = w4.cross_attention(to_dev_bf16(q), to_dev_bf16(kd), to_dev_bf16(vd), heads=heads, kv_heads=kv_heads, batch=batch,
+                           kv_batch=kv_batch, kv_len=None if n is None else torch.from_numpy(n).cuda(),
+                           key_mask=None if mask is None else torch.from_numpy(mask).cuda())
+    want, avg = oblock.cross_attention(q, k, v, heads, kv_heads, batch, kv_batch, kv_len=n, key_mask=mask)
+    err = np.abs(from_dev_bf16(O) - want)
+    bound = BF16 * np.abs(want) + (2.0 ** -8 + 2.0 ** -12) * avg
+    assert np.all(err <= bound)
