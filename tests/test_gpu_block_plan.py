@@ -104,3 +104,35 @@ def test_cross_attention_of_shared_states(w4, batch, kv_batch, sq, sk, heads, kv
     err = np.abs(from_dev_bf16(O) - want)
     bound = BF16 * np.abs(want) + (2.0 ** -8 + 2.0 ** -12) * avg
     assert np.all(err <= bound)
+
+
+def test_norm_is_what_a_w4a4_layer_reads(w4):
+    """A W4A4 layer behind the norm, against the same layer behind the oracle's
+    norm in bf16.
+
+    The kernel's norm is off by at most 2^-18 before its rounding, so it can
+    differ from the oracle's bf16 only where that lies within 2^-18 of a
+    border between values 2^-8 apart: fewer than one element in 256, by one
+    step.  Such an element moves its code by one step at most and, as the
+    largest of its block, the scale of 16: with half of the value each, the
+    outputs are off by less than sqrt(16 / 256) / 2 = 1/8 of their norm.  A norm
+    without its weight (here from 0.1 to 10) or with a wrong row factor is off
+    by about all of it.
+    """
+    import torch
+    g = rng(57)
+    x = bf16_round((g.standard_normal((300, 512)) * np.exp(g.standard_normal((300, 1)))).astype(np.float32))
+    r = bf16_round(g.standard_normal((300, 512)).astype(np.float32))
+    nw = bf16_round((10.0 ** g.uniform(-1, 1, 512)).astype(np.float32))
+    normed = torch.empty(300, 512, dtype=torch.bfloat16, device="cuda")
+    w4.rms_norm_fp8(to_dev_bf16(x), to_dev_bf16(nw), residual=to_dev_bf16(r), normed=normed)
+    want = bf16_round(oblock.rms_norm(x, r, nw)[1].astype(np.float32))
+    off = from_dev_bf16(normed) != want
+    assert np.mean(off) < 1 / 256
+    np.testing.assert_allclose(from_dev_bf16(normed), want, rtol=2 * BF16)
+    w = w4.pack_weight(to_dev_f32((0.05 * g.standard_normal((256, 512))).astype(np.float32)))
+    y = from_dev_bf16(w4.gemm(w4.quantize_act(normed), w)).astype(np.float64)
+    ref = from_dev_bf16(w4.gemm(w4.quantize_act(to_dev_bf16(want)), w)).astype(np.float64)
+    plain = from_dev_bf16(w4.gemm(w4.quantize_act(to_dev_bf16(bf16_round((x + r).astype(np.float32)))), w))
+    assert np.linalg.norm(y - ref) <= np.linalg.norm(ref) / 8
+    assert np.linalg.norm(plain - ref) >= np.linalg.norm(ref) / 2  # (the test can tell)
