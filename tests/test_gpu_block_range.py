@@ -230,3 +230,23 @@ def test_norm_of_rows_that_are_not_numbers(w4):
             assert np.isnan(y[i, j]) and not np.delete(y[i], j).any() and s[i] == 1.0
         rest = [0, 2, 4, 6, 7, 8, 10, 11]
         np.testing.assert_allclose(y[rest], oblock.rms_norm(x[rest], eps=0.0)[1], rtol=BF16 + NORM)
+
+
+@pytest.mark.parametrize("sq,ld", [(1, 72), (3, 72), (700, 72), (2, (1 << 30) + 8)])
+@pytest.mark.parametrize("heads,kv_heads", [(1, 1), (8, 1)])
+def test_cross_attention_without_keys(w4, sq, ld, heads, kv_heads):
+    """No keys at all: zeros, whatever the output's stride, and nothing beside them."""
+    import torch
+    d = 64 // heads
+    base = torch.full((2 * sq, 72), 3.0, dtype=torch.bfloat16, device="cuda")
+    O = base
+    if ld > 72:
+        far = torch.empty(ld * (2 * sq - 1) + 72, dtype=torch.bfloat16, device="cuda")
+        O = far.as_strided((2 * sq, 72), (ld, 1))
+        O.copy_(base)
+    none = torch.empty(0, kv_heads * d, dtype=torch.bfloat16, device="cuda")
+    q = torch.full((2 * sq, 64), float("nan"), dtype=torch.bfloat16, device="cuda")
+    for kv_len in (None, torch.tensor([5, -1], dtype=torch.int32, device="cuda")):
+        w4.cross_attention(q, none, none, heads=heads, kv_heads=kv_heads, batch=2, O=O[:, :64], kv_len=kv_len)
+        assert not bool(O[:, :64].any()) and bool((O[:, 64:] == 3.0).all())
+        O.fill_(3.0)
