@@ -79,6 +79,8 @@ struct Fp8PairCfg {
   static_assert(HALF % 32 == 0 && STAGE_BYTES % 1024 == 0, "tile shape");
 };
 
+constexpr long long kFp8SettleCycles = 1 << 18;  // some 0.1 ms
+
 // Tile `tile` of a product in row and column tiles: groups of `group` row
 // tiles, each swept over all columns with the row tiles fastest, so that a
 // group's rows of A stay in L2 while W streams past them.
@@ -171,6 +173,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       if (leader) {
         const uint32_t first = it > static_cast<uint32_t>(STAGES) ? it - STAGES : 0u;
         for (uint32_t j = first; j < it; ++j) mbar_wait_drain(smem_u32(&full[j % STAGES]), (j / STAGES) & 1);
+      } else if (!ok) {
+        // after a wait that gave up the even CTA may not have counted this one's
+        // newest fills: the time in which any copy lands
+        const long long start = clock64();
+        while (clock64() - start < kFp8SettleCycles) {
+        }
       }
     }
   } else if (warp == 1) {

@@ -589,9 +589,11 @@ int w4a4_last_error(void);
  * (at least 1e6), or the default 4e9 (about two seconds at 1.9 GHz) when
  * cycles <= 0.  Applies to kernels launched on the current device after the
  * call; synchronises the device.  A short bound lets a caller detect a stuck
- * pipeline quickly; it must stay well above the longest legitimate wait (a
- * full-size TMA stage lands within microseconds).  W4A4_ERR_ARG for
- * 0 < cycles < 1e6. */
+ * pipeline quickly; it must stay well above the longest legitimate wait.  A
+ * full-size TMA stage lands within microseconds, but a kernel's epilogue waits
+ * for a whole output tile: about 0.4 us per 128 columns of K in the GEMMs and
+ * 2 us per 128 keys in the attentions, both longer where work shares the GPU.
+ * W4A4_ERR_ARG for 0 < cycles < 1e6. */
 int w4a4_set_wait_bound(int64_t cycles);
 
 /*
