@@ -40,15 +40,17 @@
 //
 // Two forms:
 //   SPLIT = false  many rows: the streams are two row tiles over the same keys,
-//                  persistent CTAs, one per SM.  Bound by the tensor pipe (76 %
-//                  busy) and the exponentials (MUFU 54 %), at full load by the
-//                  power cap: 1290 TFLOP/s back to back, 1100 sustained,
-//                  against 1646 and 1388 measured for a large matrix product.
+//                  persistent CTAs, one per SM.  Bound by the tensor pipe and
+//                  the exponentials in turn (57 and 50 % of the active cycles
+//                  under ncu), at full load by the power cap: 16384 queries x
+//                  4096 keys, 16 heads of 128, 1150 to 1240 TFLOP/s in runs of
+//                  3 ms, 1075 sustained, against 1646 and 1388 measured for a
+//                  large matrix product.
 //   SPLIT = true   few rows: the streams are the even and odd key tiles of one
 //                  row tile, and a cluster of CTAs splits the keys; the
 //                  partial sums meet in (distributed) shared memory.  Bound by
 //                  the key and value bytes and about 7 us of latency (4 x 1
-//                  query, 4109 keys, 32 heads on 8: 17.5 us, 3.85 TB/s).
+//                  query, 4109 keys, 32 heads on 8: 17.1 us, 3.94 TB/s).
 #pragma once
 
 #include "attention.cuh"

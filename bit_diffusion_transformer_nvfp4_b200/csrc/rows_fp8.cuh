@@ -12,15 +12,16 @@
 // from one pass and one reduction, and the row stays in registers: every
 // input is read once and every output written once.  That traffic (for
 // x, r, hidden and codes 7 bytes an element) is the bound: norm of 16896 x
-// 6144 109 us (6.7 TB/s), its codes alone 46.3 us (6.7 TB/s).  Short rows are
-// bound by instruction issue (36888 x 128 without a residual: 3.7 us, 3.8 TB/s).
+// 6144 107.5 us (6.8 TB/s), its codes alone 46.3 us (6.7 TB/s).  Short rows are
+// bound by instruction issue (36888 x 128 without a residual: 3.6 us, 3.9 TB/s).
 //
 // Rows whose squares leave fp32's range (|h| from about 2^52 up, or below 2^-45
 // with an eps that small) take their sum again, scaled by a power of two, from
 // the inputs: a branch that other rows do not enter (rows_far).
 //
-// Two shapes: rows of up to 2048 columns take a power of two of lanes of one
-// warp (shuffles only); wider ones a block of their own, a thread holding V
+// Two shapes: short rows (up to 1024 columns for the norm, which keeps the
+// residual too, 2048 for the codes alone) take a power of two of lanes of one
+// warp (shuffles only); wider ones a block of their own.  A thread holds V
 // 16-byte vectors of the row.
 #pragma once
 
@@ -243,9 +244,10 @@ __device__ __forceinline__ void rows_store(const RowsFp8Params& p, int64_t row, 
 }
 
 // A row per `lanes` lanes (a power of two up to 32) of a warp: no barriers, and
-// as many vectors a lane as there are up to kRowsWarpVecs, so that the
-// reduction and the row's quotients are shared by many elements (a 128-column
-// row on 16 lanes of one vector took 7.2 us for 36888 rows).
+// four vectors a lane (six or eight where that fills the warp, for the codes
+// alone), so that the reduction and the row's quotients are shared by many
+// elements (a 128-column row on 16 lanes of one vector took 7.2 us for 36888
+// rows).
 template <int V, bool NORM>
 __global__ void __launch_bounds__(kRowsWarpThreads) rows_fp8_warp_kernel(const RowsFp8Params p, int lanes) {
   grid_launch_dependents();

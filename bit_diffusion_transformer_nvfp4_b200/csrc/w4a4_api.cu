@@ -726,7 +726,7 @@ int launch_rows_fp8(const RowsFp8Params& p, cudaStream_t stream) {
     // a row per group of lanes: four vectors a lane while that fills no warp.
     // (Up to 2048 columns for the codes alone, 9000 x 1032: 5.7 us against 9.9
     // with a block a row; the norm keeps the residual too and gains only up
-    // to 1024 columns, 9000 x 2048: 29.9 us against 22.7.)
+    // to 1024 columns, 9000 x 2048: 26.1 us against 20.8.)
     int lanes = 1;
     while (lanes < 32 && 4 * lanes < nv) lanes *= 2;
     cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(p.rows, kRowsWarpThreads / lanes)), 1, 1);
@@ -741,7 +741,7 @@ int launch_rows_fp8(const RowsFp8Params& p, cudaStream_t stream) {
   } else {
     // a row per block of up to 512 threads: four vectors a thread, eight for
     // wide rows (codes of 2000 x 16384: 16.6 us with eight, 18.1 with four;
-    // norm of 1000 x 16384: 29.2 us with eight, 23.4 with four)
+    // norm of 1000 x 16384: 28.3 us with eight, 20.8 with four)
     const int vecs = nv <= (NORM ? 2048 : 1024) ? 4 : 8;
     cfg.gridDim = dim3(static_cast<unsigned>(p.rows), 1, 1);
     cfg.blockDim = dim3(static_cast<unsigned>(ceil_div(ceil_div(nv, vecs), 32) * 32), 1, 1);

@@ -486,9 +486,11 @@ int fp8_gemm(const uint8_t* A8, int64_t lda, const float* s_a, int s_a_rows, int
  *   O     out bf16 [batch * Sq, ldo]
  * Keys that do not count may hold anything, NaN included.  A query without a
  * key gets 0.  A counted score that is NaN or +infinity makes its row NaN;
- * one of -infinity weighs nothing (a row of nothing else is 0).
- * fp32 scores, sums and accumulation; the probabilities are rounded to bf16
- * for the second product.  Strides are in elements, multiples of 8 (ld_mask:
+ * finite ones may be of any size; one of -infinity weighs nothing (at most
+ * 2^-126 of the row's largest weight; a row of nothing else is 0).
+ * fp32 scores, sums and accumulation; the probabilities, up to 2^9 of the
+ * weight they stand for, are rounded to bf16 for the second product: finite
+ * outputs want |value| times the keys that count below 2^119.  Strides are in elements, multiples of 8 (ld_mask:
  * any, >= Skv); Sq, Skv <= 2^24, batch and heads <= 65535, batch * heads *
  * ceil(Sq / 4) <= 2^30, a sequence's rows below 2^39 elements.  No workspace;
  * results do not depend on timing.
