@@ -1290,6 +1290,8 @@ int rmsnorm_fp8(const void* X, int64_t rows, int64_t cols, int64_t ldx, const vo
   if (!(eps >= 0.0f) || !(eps < 3.0e38f)) return W4A4_ERR_ARG;
   if (rows == 0) return W4A4_OK;
   if (!codes && !normed) return W4A4_ERR_NULL;
+  // in place row by row, or rows would be overwritten before they are read
+  if (hidden && rows > 1 && ((hidden == X && ldh != ldx) || (hidden == R && ldh != ldr))) return W4A4_ERR_ARG;
   if (!aligned16(R) || !aligned16(weight) || !aligned16(hidden) || !aligned16(normed)) return W4A4_ERR_ALIGN;
   DeviceInfo* dev = nullptr;
   st = device_setup(&dev);
@@ -1328,6 +1330,7 @@ int fp8_gemm(const uint8_t* A8, int64_t lda, const float* s_a, int s_a_rows, int
     return W4A4_ERR_ARG;
   if (M == 0) return W4A4_OK;
   if (!A8 || !s_a || !W8 || !s_w || !Y) return W4A4_ERR_NULL;
+  if (R == Y && ldr != ldy && M > 1) return W4A4_ERR_ARG;  // in place, or not at all
   if (!aligned16(A8) || !aligned16(W8) || !aligned16(s_w) || !aligned16(bias) || !aligned16(R) || !aligned16(Y) ||
       reinterpret_cast<uintptr_t>(s_a) % 4 != 0)
     return W4A4_ERR_ALIGN;

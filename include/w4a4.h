@@ -435,7 +435,7 @@ int fp8_quantize_rows(const void* X, int64_t rows, int64_t cols, int64_t ldx, ui
  *   X, R      in  bf16 [rows, ldx / ldr] (R NULL: no addition)
  *   weight    in  bf16 [cols] or NULL (ones);  eps finite and >= 0
  *   hidden    out bf16(h) [rows, ldh] or NULL; may be X or R itself (same
- *                 pointer and stride)
+ *                 pointer and stride; W4A4_ERR_ARG for another stride)
  *   normed    out bf16(y) [rows, ldn] or NULL (the input of
  *                 nvfp4_quantize_act, for a W4A4 layer after the norm)
  *   codes, scales  out as in fp8_quantize_rows; codes NULL: neither is
@@ -458,8 +458,9 @@ int rmsnorm_fp8(const void* X, int64_t rows, int64_t cols, int64_t ldx, const vo
  *   W8   in  E4M3 [N, ldw bytes];  s_w fp32 [N], 16-byte aligned
  *   bias in  bf16 [N] or NULL;  epilogue: W4A4_EPI_NONE or W4A4_EPI_GELU_TANH
  *   R    in  bf16 [M, ldr] residual or NULL; may be Y itself (same pointer
- *            and stride)
+ *            and stride; W4A4_ERR_ARG for another stride)
  *   Y    out bf16 [M, ldy]
+ * The sum is multiplied with s_a[m] first, then with s_w[n], each in fp32.
  *   K % 16 == 0, K <= W4A4_MAX_K, N % 8 == 0, lda / ldw % 16 == 0, ldr / ldy % 8 == 0
  * Up to 16 rows, and up to 128 where it is faster: the weight streams past the
  * tokens, K split over a cluster of CTAs whose partial sums are added in slice

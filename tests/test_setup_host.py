@@ -71,3 +71,32 @@ def test_set_up_of_one_operator_is_not_the_others(tmp_path, how):
     run = subprocess.run([sys.executable, "-c", PROGRAM, str(fake), lib, how], capture_output=True, text=True, timeout=120,
                          env={**os.environ, "LD_PRELOAD": str(fake)})
     assert run.returncode == 0 and run.stdout == "ok\n", run.stdout + run.stderr
+
+
+def test_in_place_with_another_stride_is_refused():
+    """A residual sum or an output over its own input needs the input's rows:
+    another stride would overwrite rows before they are read."""
+    import ctypes
+    from ctypes import c_float, c_int64 as i64
+    so = ctypes.CDLL(build.build())
+    P, Q = ctypes.c_void_p(1 << 20), ctypes.c_void_p(1 << 21)
+    ARG = -8
+
+    def norm(x, r, hidden, ldx, ldr, ldh, rows=4):
+        return so.rmsnorm_fp8(x, i64(rows), i64(64), i64(ldx), r, i64(ldr), None, c_float(1e-6), hidden, i64(ldh), None,
+                              i64(0), ctypes.c_void_p(1 << 22), i64(64), ctypes.c_void_p(1 << 23), None)
+
+    def linear(r, y, ldr, ldy, rows=4):
+        return so.fp8_gemm(P, i64(64), P, 1, i64(rows), i64(64), i64(64), P, i64(64), P, None, 0, r, i64(ldr), y,
+                           i64(ldy), None)
+
+    assert norm(P, Q, P, 72, 64, 64) == ARG and norm(Q, P, P, 64, 72, 64) == ARG
+    assert norm(P, None, P, 72, 0, 64) == ARG
+    assert linear(Q, Q, 72, 64) == ARG and linear(Q, Q, 64, 72) == ARG
+    # allowed: the same rows, other memory, one row (asked only where no kernel
+    # can start: the addresses are made up)
+    if not __import__("torch").cuda.is_available():
+        for st in (norm(P, Q, P, 72, 64, 72), norm(Q, P, P, 64, 72, 72), norm(P, Q, None, 72, 64, 0),
+                   norm(P, Q, P, 72, 64, 64, rows=1), linear(Q, Q, 72, 72), linear(P, Q, 72, 64),
+                   linear(Q, Q, 72, 64, rows=1)):
+            assert st == -4
